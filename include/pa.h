@@ -83,8 +83,9 @@ enum {
     PA_DEVERR_BLOCK_ID = 2,  /* block table / block mapping id outside [0, num_blocks) */
     PA_DEVERR_CONTEXT = 4,   /* context length < 0, > max_context_len, or beyond the block table */
     PA_DEVERR_QUERY = 8,     /* query_start_loc not monotone, or a chunk longer than its context */
-    PA_DEVERR_TIMEOUT = 16   /* a bounded wait inside a kernel gave up (internal error; the
+    PA_DEVERR_TIMEOUT = 16,  /* a bounded wait inside a kernel gave up (internal error; the
                                 kernel returned instead of hanging) */
+    PA_DEVERR_AXIS = 32      /* pa_rope_axes.pair_axis entry outside [0, num_axes) */
 };
 
 /*
@@ -325,6 +326,103 @@ int pa_decode_rope(void *out, pa_dtype out_dtype, const void *query, const void 
                    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
                    pa_dtype kv_dtype, const pa_rope *rope, void *workspace, size_t workspace_bytes,
                    int32_t *status, pa_stream_t stream);
+
+/*
+ * Sliding-window attention with sinks.  A query at position p (its sequence's keys are at
+ * positions 0, 1, ...) sees the keys j <= p with j > p - window (the newest `window` keys,
+ * its own included) or j < num_sinks (the first tokens of the sequence, which stay visible).
+ * window >= context length makes it plain causal attention; num_sinks = 0 leaves the bare
+ * window.  Layouts, checks, errors and asynchrony are those of pa_decode / pa_prefill_chunk,
+ * with two differences:
+ *  - a block-table entry is read only if its block holds a key that some query row of the
+ *    sequence sees: the blocks behind the window may have been freed, their entries hold
+ *    anything (-1, say).  What the cache holds in slots that no row of the sequence sees is
+ *    never used, not even NaN;
+ *  - there is no workspace: the pieces of a split context are merged inside the launch.
+ * window < 1 or num_sinks < 0 returns PA_ERR_INVALID_ARG.
+ */
+
+/*
+ * pa_decode_window -- decode attention (one query token per sequence, at position
+ * context_lens[s] - 1) over the window and the sinks.  Arguments as for pa_decode; F32, F16
+ * and BF16 caches.  A sequence with context length 0 gets an all-zero row; a negative
+ * context, or one past max_context_len or the block table, is reported and clamped, as in
+ * pa_decode.  fp32 accumulation; a row does not depend on the rest of the batch while the
+ * batch size stays the same.
+ */
+int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const void *key_cache,
+                     const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int max_context_len, int window, int num_sinks,
+                     int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                     int num_blocks, float scale, pa_dtype kv_dtype, int32_t *status,
+                     pa_stream_t stream);
+
+/*
+ * pa_prefill_window -- chunked prefill under the window: row i of sequence s sits at
+ * position context_lens[s] - Lq_s + i.  Arguments, invalid chunks and dtypes (F16, BF16) as
+ * for pa_prefill_chunk.  Values at the positions that some row of a chunk sees must be
+ * finite (a key that one row sees and another does not enters the second row's sum with
+ * weight zero).
+ */
+int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
+                      const int32_t *query_start_loc, int num_tokens, int max_query_len,
+                      const void *key_cache, const void *value_cache, const int32_t *block_tables,
+                      int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
+                      int window, int num_sinks, int num_seqs, int num_heads, int num_kv_heads,
+                      int head_dim, int block_size, int num_blocks, float scale, pa_dtype kv_dtype,
+                      int32_t *status, pa_stream_t stream);
+
+/*
+ * Rotary positions with several axes (time, height and width of images and video): every
+ * rotated pair belongs to one axis and turns by that axis's position of the token.
+ */
+#define PA_ROPE_MAX_AXES 8
+typedef struct {
+    const float *freqs;       /* device, [rope_dim / 2]: angular frequency of pair i (pa_rope_yarn_freqs) */
+    const int32_t *pair_axis; /* device, [rope_dim / 2]: axis of pair i, 0 .. num_axes - 1 (pa_rope_pair_axes) */
+    int rope_dim;             /* even, 2 .. head_dim */
+    int num_axes;             /* 1 .. PA_ROPE_MAX_AXES */
+    int halves;               /* 0: pair i is elements (2i, 2i+1); 1: elements (i, i + rope_dim/2) */
+} pa_rope_axes;
+
+/*
+ * pa_rope_pair_axes -- host: the axis of each of the rope_dim / 2 pairs from the number of
+ * pairs of each axis (sections, which must add up to rope_dim / 2): interleaved = 0 gives
+ * axis 0 the first sections[0] pairs, axis 1 the next sections[1], and so on; interleaved = 1
+ * deals the pairs out in turn (0, 1, 2, 0, 1, 2, ...), passing over an axis that has all of
+ * its pairs.
+ */
+int pa_rope_pair_axes(int32_t *pair_axis, int rope_dim, const int32_t *sections, int num_axes,
+                      int interleaved);
+
+/*
+ * pa_reshape_and_cache_rope_axes -- one step's rotation and cache write in one launch:
+ * queries rotated into query_out, keys rotated into their cache slots, values copied into
+ * theirs.
+ *
+ *   query_out  [num_tokens][num_heads][head_dim], kv_dtype (written, dense); may be `query`
+ *              itself when query_stride is num_heads * head_dim
+ *   query      num_tokens rows [num_heads][head_dim], query_stride elements apart
+ *   key, value num_tokens rows [num_kv_heads][head_dim], key_stride / value_stride apart
+ *   positions  int32 [num_axes][num_tokens]: position of token t on each axis
+ *   slot_mapping, caches  as for pa_reshape_and_cache (a slot < 0 writes no key and value;
+ *              the token's query is rotated all the same)
+ *
+ * Strides are in elements, at least the row and a multiple of 16 bytes (so the three may be
+ * slices of one projection's output).  num_heads = 0 (query and query_out NULL) rotates and
+ * writes keys only.  Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i], the
+ * angle formed exactly and reduced to [-pi, pi] in fp32 (positions below 2^24 in magnitude),
+ * rotation in fp32, rounded once; elements past rope_dim and values are bit copies.  A
+ * pair_axis entry outside [0, num_axes) is reported (PA_DEVERR_AXIS) and its pair not
+ * rotated.
+ */
+int pa_reshape_and_cache_rope_axes(void *query_out, const void *query, const void *key,
+                                   const void *value, void *key_cache, void *value_cache,
+                                   const int64_t *slot_mapping, const int32_t *positions,
+                                   int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                   int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                   int block_size, int num_blocks, pa_dtype kv_dtype,
+                                   const pa_rope_axes *rope, int32_t *status, pa_stream_t stream);
 
 /* Static description of a PA_* return code. */
 const char *pa_status_string(int code);

@@ -56,3 +56,24 @@ def q_scale(positions, beta: float, orig_ctx: int) -> np.ndarray:
     if orig_ctx <= 0:
         return np.ones(pos.shape, dtype=np.float64)
     return 1.0 + beta * np.log1p((pos // orig_ctx).astype(np.float64))
+
+
+def pair_axes(rope_dim: int, sections, interleaved: bool = False) -> np.ndarray:
+    """Axis of each pair: ``sections[a]`` pairs for axis a, in order, or dealt out in turn."""
+    if not interleaved:
+        return np.repeat(np.arange(len(sections)), sections).astype(np.int32)
+    rounds = [a for r in range(max(sections)) for a, n in enumerate(sections) if r < n]
+    return np.array(rounds, dtype=np.int32)
+
+
+def apply_rope_axes(x: np.ndarray, positions, freqs: np.ndarray, axes, halves: bool) -> np.ndarray:
+    """Rotate rows ``x[t][h][:]`` (returned in fp64): pair i turns by ``positions[axes[i]][t] * freqs[i]``;
+    it is elements (i, i + len(axes)) with ``halves``, else (2i, 2i + 1)."""
+    y = np.array(x, dtype=np.float64, copy=True)
+    pos = np.asarray(positions, dtype=np.float64)
+    for i, a in enumerate(axes):
+        z = np.exp(1j * pos[a] * float(freqs[i]))[:, None]
+        u, w = (i, i + len(axes)) if halves else (2 * i, 2 * i + 1)
+        both = (y[:, :, u] + 1j * y[:, :, w]) * z
+        y[:, :, u], y[:, :, w] = both.real, both.imag
+    return y

@@ -15,7 +15,11 @@ Operations (see ``include/pa.h`` for layouts, ownership and error behaviour):
 * ``pa_copy_blocks`` -- whole-block copies for prefix-cache reuse;
 * ``pa_reshape_and_cache_rope`` / ``pa_decode_rope`` -- the same with rotary position
   embedding (GPT-J pairs, YaRN table from ``pa_rope_yarn_freqs``) fused into the key write
-  and the decode query load.
+  and the decode query load;
+* ``pa_decode_window`` / ``pa_prefill_window`` -- the attention over a sliding window and the
+  first tokens (sinks);
+* ``pa_reshape_and_cache_rope_axes`` -- a step's queries and keys rotated with several position
+  axes (``RopeAxes``, ``pa_rope_pair_axes``), keys and values written to their slots.
 """
 from __future__ import annotations
 
@@ -29,6 +33,7 @@ __all__ = [
     "PAError", "pa_reshape_and_cache", "pa_decode_workspace_size", "pa_decode", "pa_decode_noalloc",
     "pa_prefill_chunk", "pa_copy_blocks", "pa_status_string", "pa_version", "library_path",
     "Rope", "pa_rope_yarn_freqs", "pa_reshape_and_cache_rope", "pa_decode_rope", "pa_decode_write",
+    "pa_decode_window", "pa_prefill_window", "RopeAxes", "pa_rope_pair_axes", "pa_reshape_and_cache_rope_axes",
     "PA_F32", "PA_F16", "PA_BF16",
 ]
 
@@ -70,9 +75,25 @@ _lib.pa_reshape_and_cache_rope.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _
                                            ctypes.POINTER(_PaRope), _vp, _vp]
 _lib.pa_decode_rope.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                 _i32, _i32, _f32, _i32, ctypes.POINTER(_PaRope), _vp, _sz, _vp, _vp]
+
+
+class _PaRopeAxes(ctypes.Structure):
+    _fields_ = [("freqs", _vp), ("pair_axis", _vp), ("rope_dim", _i32), ("num_axes", _i32), ("halves", _i32)]
+
+
+_i64 = ctypes.c_int64
+_lib.pa_decode_window.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+                                  _i32, _i32, _i32, _f32, _i32, _vp, _vp]
+_lib.pa_prefill_window.argtypes = [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                   _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp]
+_lib.pa_rope_pair_axes.argtypes = [_vp, _i32, _vp, _i32, _i32]
+_lib.pa_reshape_and_cache_rope_axes.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
+                                                _i64, _i64, _i64, _i32, _i32, _i32, ctypes.POINTER(_PaRopeAxes),
+                                                _vp, _vp]
 for _name in ("pa_reshape_and_cache", "pa_decode", "pa_decode_noalloc", "pa_prefill_chunk",
               "pa_copy_blocks", "pa_version", "pa_rope_yarn_freqs", "pa_reshape_and_cache_rope",
-              "pa_decode_rope", "pa_decode_write"):
+              "pa_decode_rope", "pa_decode_write", "pa_decode_window", "pa_prefill_window",
+              "pa_rope_pair_axes", "pa_reshape_and_cache_rope_axes"):
     getattr(_lib, _name).restype = _i32
 
 
@@ -247,3 +268,142 @@ def pa_decode_rope(out, query, key_cache, value_cache, block_tables, context_len
                                int(max_context_len), S, Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache),
                                ctypes.byref(r), _ptr(workspace), ws_bytes, _ptr(status), _stream(stream)),
            "pa_decode_rope")
+
+
+# ----------------------------------------------------------------------------- sliding window
+
+def _require(ok: bool, what: str, why: str) -> None:
+    if not ok:
+        raise PAError(-1, f"{what}: {why}")
+
+
+def _run_on(dev: torch.device, stream, call):
+    """``call(stream handle)`` with the tensors' device current (a stream given must be of it)."""
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def _check_window(what, out, query, key_cache, value_cache, block_tables, ints, status) -> None:
+    """Shapes, types, layout and device of the windowed calls' tensors (``ints``: int32 vectors)."""
+    _require(query.dim() == 3 and key_cache.dim() == 4 and block_tables.dim() == 2, what,
+             "query is [T][Hq][D], a cache [NB][bs][Hkv][D], block_tables [S][max_blocks]")
+    _require(out.shape == query.shape and key_cache.shape == value_cache.shape and query.shape[2] == key_cache.shape[3],
+             what, "out is shaped as query, value_cache as key_cache, head dims are equal")
+    _require(query.dtype == key_cache.dtype == value_cache.dtype, what, "query and caches share one dtype")
+    _require(block_tables.dtype == torch.int32 and all(t.dtype == torch.int32 and t.dim() == 1 for t in ints) and
+             (status is None or status.dtype == torch.int32), what,
+             "tables, lengths, starts and status are int32")
+    dev = query.device
+    ts = (out, query, key_cache, value_cache, block_tables, *ints) if status is None else (
+        out, query, key_cache, value_cache, block_tables, status, *ints)
+    _require(all(t.is_contiguous() for t in ts), what, "tensors must be contiguous")
+    _require(dev.type == "cuda" and all(t.device == dev for t in ts), what, "tensors must be on one CUDA device")
+
+
+def pa_decode_window(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len: int,
+                     window: int, num_sinks: int, scale: float, *, status=None, stream=None) -> None:
+    """pa_decode over the newest ``window`` keys and the first ``num_sinks`` of each sequence.
+    No workspace; table entries of blocks that no key is seen in are not read."""
+    _check_window("pa_decode_window", out, query, key_cache, value_cache, block_tables, (context_lens,), status)
+    S, Hq, D = query.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    _require(block_tables.shape[0] == S == context_lens.shape[0], "pa_decode_window",
+             "one query row, table row and context length per sequence")
+    _check(_run_on(query.device, stream, lambda st: _lib.pa_decode_window(
+        _ptr(out), _dt(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(context_lens), int(max_context_len), int(window), int(num_sinks), S, Hq, Hkv, D,
+        bs, NB, float(scale), _dt(key_cache), _ptr(status), st)), "pa_decode_window")
+
+
+def pa_prefill_window(out, query, query_start_loc, max_query_len: int, key_cache, value_cache, block_tables,
+                      context_lens, max_context_len: int, window: int, num_sinks: int, scale: float, *, status=None,
+                      stream=None) -> None:
+    """pa_prefill_chunk over the newest ``window`` keys before each row and the first ``num_sinks``."""
+    _check_window("pa_prefill_window", out, query, key_cache, value_cache, block_tables,
+                  (context_lens, query_start_loc), status)
+    Tq, Hq, D = query.shape
+    NB, bs, Hkv, _ = key_cache.shape
+    S = context_lens.shape[0]
+    _require(block_tables.shape[0] == S and query_start_loc.shape[0] == S + 1, "pa_prefill_window",
+             "one table row per sequence, S + 1 row starts")
+    _check(_run_on(query.device, stream, lambda st: _lib.pa_prefill_window(
+        _ptr(out), _dt(out), _ptr(query), _ptr(query_start_loc), Tq, int(max_query_len), _ptr(key_cache),
+        _ptr(value_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), int(max_context_len),
+        int(window), int(num_sinks), S, Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache), _ptr(status), st)),
+        "pa_prefill_window")
+
+
+# ----------------------------------------------------------------------------- rotary axes
+
+def pa_rope_pair_axes(rope_dim: int, sections, interleaved: bool = False):
+    """The axis of each rotated pair (host, int32 ``[rope_dim / 2]``) from the pairs per axis:
+    in order, or with ``interleaved`` dealt out in turn."""
+    import numpy as np
+    sec = np.ascontiguousarray(sections, dtype=np.int32)
+    out = np.empty(max(0, rope_dim // 2), dtype=np.int32)
+    _check(_lib.pa_rope_pair_axes(out.ctypes.data, int(rope_dim), sec.ctypes.data, int(sec.size), int(interleaved)),
+           "pa_rope_pair_axes")
+    return out
+
+
+class RopeAxes:
+    """Arguments of the multi-axis rotation: device tensors ``freqs`` (fp32) and ``pair_axis``
+    (int32), both ``[rope_dim / 2]``, the number of axes, and whether pair i is the elements
+    (i, i + rope_dim / 2) (``halves``) or (2i, 2i + 1)."""
+
+    def __init__(self, freqs: torch.Tensor, pair_axis: torch.Tensor, rope_dim: int, num_axes: int,
+                 halves: bool = False):
+        _require(freqs.dtype == torch.float32 and pair_axis.dtype == torch.int32 and freqs.is_contiguous() and
+                 pair_axis.is_contiguous() and 2 * freqs.numel() == rope_dim == 2 * pair_axis.numel() and
+                 freqs.device == pair_axis.device, "RopeAxes",
+                 "freqs is fp32 and pair_axis int32, both [rope_dim / 2], dense, on one device")
+        self.freqs, self.pair_axis = freqs, pair_axis
+        self.rope_dim, self.num_axes, self.halves = int(rope_dim), int(num_axes), bool(halves)
+
+    def _c(self):
+        return _PaRopeAxes(self.freqs.data_ptr(), self.pair_axis.data_ptr(), self.rope_dim, self.num_axes,
+                           int(self.halves))
+
+
+def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
+                                   rope: RopeAxes, *, status=None, stream=None) -> None:
+    """query ``[T][Hq][D]`` rotated into ``query_out`` (dense; may be ``query``), key ``[T][Hkv][D]``
+    rotated and value copied into the pools at ``slot_mapping`` (int64 [T]), at ``positions``
+    (int32 [num_axes][T]).  query, key and value may be slices of wider rows.  ``query`` and
+    ``query_out`` None: keys and values only."""
+    what = "pa_reshape_and_cache_rope_axes"
+    _require((query is None) == (query_out is None), what, "query and query_out go together")
+    _require(key.dim() == 3 and key.shape == value.shape and key_cache.dim() == 4 and
+             key_cache.shape == value_cache.shape and key.shape[1:] == key_cache.shape[2:], what,
+             "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
+    T, Hkv, D = key.shape
+    NB, bs = key_cache.shape[:2]
+    rows, dense = [key, value], [key_cache, value_cache, slot_mapping, positions]
+    Hq = 0
+    if query is not None:
+        _require(query.dim() == 3 and query.shape == query_out.shape and query.shape[0] == T and query.shape[2] == D,
+                 what, "query and query_out are [T][Hq][D]")
+        Hq = query.shape[1]
+        rows.append(query)
+        dense.append(query_out)
+        _require(query_out.dtype == query.dtype == key.dtype, what, "query, keys and caches share one dtype")
+    if status is not None:
+        dense.append(status)
+    _require(key.dtype == value.dtype == key_cache.dtype == value_cache.dtype, what,
+             "query, keys, values and caches share one dtype")
+    _require(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,) and positions.dtype == torch.int32 and
+             positions.shape == (rope.num_axes, T) and (status is None or status.dtype == torch.int32), what,
+             "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32")
+    _require(all(t.is_contiguous() for t in dense), what, "caches, query_out, slots and positions must be contiguous")
+    _require(T == 0 or all(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D) for t in rows), what,
+             "a token's heads must be contiguous")
+    dev = key.device
+    _require(dev.type == "cuda" and rope.freqs.device == dev and all(t.device == dev for t in rows) and
+             all(t.device == dev for t in dense), what, "tensors must be on one CUDA device")
+    r = rope._c()
+    _check(_run_on(dev, stream, lambda st: _lib.pa_reshape_and_cache_rope_axes(
+        _ptr(query_out), _ptr(query), _ptr(key), _ptr(value), _ptr(key_cache), _ptr(value_cache),
+        _ptr(slot_mapping), _ptr(positions), T, Hq, Hkv, D, 0 if query is None else query.stride(0), key.stride(0),
+        value.stride(0), bs, NB, _dt(key_cache), ctypes.byref(r), _ptr(status), st)), what)

@@ -213,6 +213,8 @@ struct DecodeArgs {
     // the new token of every sequence, written to its slot first (null key: no write)
     const void *new_key = nullptr, *new_value = nullptr;
     const int64_t *slot_mapping = nullptr;
+    // sliding window (0: none) and the first tokens that stay visible
+    int window = 0, num_sinks = 0;
 };
 
 struct PrefillArgs {
@@ -233,6 +235,22 @@ struct PrefillArgs {
     int32_t *status;
     cudaStream_t stream;
     int decode_rows = 0;  // one query row per sequence (token s), no query_start_loc
+    int window = 0, num_sinks = 0;  // sliding window (0: none) and the first tokens that stay visible
+};
+
+struct RopeAxesArgs {
+    void *query_out;
+    const void *query, *key, *value;
+    void *key_cache, *value_cache;
+    const int64_t *slot_mapping;
+    const int32_t *positions;
+    int num_tokens, num_heads, num_kv_heads, head_dim;
+    int64_t query_stride, key_stride, value_stride;
+    int block_size, num_blocks;
+    pa_dtype kv_dtype;
+    pa_rope_axes rope;
+    int32_t *status;
+    cudaStream_t stream;
 };
 
 int launch_reshape_and_cache(const void *key, const void *value, void *key_cache,
@@ -251,5 +269,8 @@ size_t decode_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads, int
                               int max_context_len);
 int launch_decode(const DecodeArgs &a);
 int launch_prefill(const PrefillArgs &a);
+int launch_decode_window(const DecodeArgs &a);
+int launch_prefill_window(const PrefillArgs &a);
+int launch_reshape_and_cache_rope_axes(const RopeAxesArgs &a);
 
 }  // namespace pa

@@ -245,4 +245,116 @@ int pa_prefill_chunk(void *out, pa_dtype out_dtype, const void *query,
     return pa::launch_prefill(a);
 }
 
+int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const void *key_cache,
+                     const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *context_lens, int max_context_len, int window, int num_sinks,
+                     int num_seqs, int num_heads, int num_kv_heads, int head_dim, int block_size,
+                     int num_blocks, float scale, pa_dtype kv_dtype, int32_t *status,
+                     pa_stream_t stream) {
+    int rc = check_attention(out, out_dtype, query, key_cache, value_cache, block_tables,
+                             max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                             kv_dtype);
+    if (rc != PA_OK) return rc;
+    if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return PA_OK;
+    if (!aligned(status, 4)) return PA_ERR_INVALID_ARG;
+    pa::DecodeArgs a{out,          out_dtype,      query,     key_cache,    value_cache,
+                     block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                     num_seqs,     num_heads,      num_kv_heads, head_dim,  block_size,
+                     num_blocks,   scale,          kv_dtype,  nullptr,      0,
+                     status,       reinterpret_cast<cudaStream_t>(stream)};
+    a.window = window;
+    a.num_sinks = num_sinks;
+    return pa::launch_decode_window(a);
+}
+
+int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
+                      const int32_t *query_start_loc, int num_tokens, int max_query_len,
+                      const void *key_cache, const void *value_cache, const int32_t *block_tables,
+                      int max_blocks_per_seq, const int32_t *context_lens, int max_context_len,
+                      int window, int num_sinks, int num_seqs, int num_heads, int num_kv_heads,
+                      int head_dim, int block_size, int num_blocks, float scale, pa_dtype kv_dtype,
+                      int32_t *status, pa_stream_t stream) {
+    int rc = check_attention(out, out_dtype, query, key_cache, value_cache, block_tables,
+                             max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                             kv_dtype);
+    if (rc != PA_OK) return rc;
+    if (kv_dtype == PA_F32) return PA_ERR_UNSUPPORTED;
+    if (num_tokens < 0 || max_query_len < 0 || window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+    if (!query_start_loc || !aligned(query_start_loc, 4) || !aligned(status, 4))
+        return PA_ERR_INVALID_ARG;
+    pa::PrefillArgs a{out,          out_dtype,  query,        query_start_loc,   num_tokens,
+                      max_query_len, key_cache, value_cache,  block_tables,      max_blocks_per_seq,
+                      context_lens, max_context_len, num_seqs, num_heads,        num_kv_heads,
+                      head_dim,     block_size, num_blocks,   scale,             kv_dtype,
+                      status,       reinterpret_cast<cudaStream_t>(stream)};
+    a.window = window;
+    a.num_sinks = num_sinks;
+    return pa::launch_prefill_window(a);
+}
+
+int pa_rope_pair_axes(int32_t *pair_axis, int rope_dim, const int32_t *sections, int num_axes,
+                      int interleaved) {
+    if (!pair_axis || !sections || rope_dim < 2 || rope_dim % 2 != 0 || num_axes < 1 || num_axes > PA_ROPE_MAX_AXES)
+        return PA_ERR_INVALID_ARG;
+    const int pairs = rope_dim / 2;
+    int left[PA_ROPE_MAX_AXES];
+    int64_t sum = 0;
+    for (int a = 0; a < num_axes; ++a) {
+        if (sections[a] < 0) return PA_ERR_INVALID_ARG;
+        left[a] = sections[a];
+        sum += sections[a];
+    }
+    if (sum != pairs) return PA_ERR_INVALID_ARG;
+    for (int i = 0, a = 0; i < pairs; ++i) {
+        while (left[a] == 0) a = (a + 1) % num_axes;
+        pair_axis[i] = a;
+        --left[a];
+        if (interleaved) a = (a + 1) % num_axes;
+    }
+    return PA_OK;
+}
+
+int pa_reshape_and_cache_rope_axes(void *query_out, const void *query, const void *key,
+                                   const void *value, void *key_cache, void *value_cache,
+                                   const int64_t *slot_mapping, const int32_t *positions,
+                                   int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                                   int64_t query_stride, int64_t key_stride, int64_t value_stride,
+                                   int block_size, int num_blocks, pa_dtype kv_dtype,
+                                   const pa_rope_axes *rope, int32_t *status, pa_stream_t stream) {
+    const int eb = elem_bytes(kv_dtype);
+    if (!eb || num_tokens < 0 || num_heads < 0 || num_kv_heads <= 0 || num_blocks < 0 || num_heads > 65535 ||
+        num_kv_heads > 65535)
+        return PA_ERR_INVALID_ARG;
+    if (!head_dim_ok(head_dim) || !block_size_ok(block_size)) return PA_ERR_UNSUPPORTED;
+    if (!rope || !rope->freqs || !rope->pair_axis || !aligned(rope->freqs, 4) || !aligned(rope->pair_axis, 4))
+        return PA_ERR_INVALID_ARG;
+    if (rope->rope_dim < 2 || rope->rope_dim % 2 != 0 || rope->rope_dim > head_dim || rope->num_axes < 1 ||
+        rope->num_axes > PA_ROPE_MAX_AXES || (rope->halves != 0 && rope->halves != 1))
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!key || !value || !key_cache || !value_cache || !slot_mapping || !positions) return PA_ERR_INVALID_ARG;
+    if (num_heads ? (!query || !query_out) : (query || query_out)) return PA_ERR_INVALID_ARG;
+    if (!aligned(query_out, 16) || !aligned(query, 16) || !aligned(key, 16) || !aligned(value, 16) ||
+        !aligned(key_cache, 16) || !aligned(value_cache, 16) || !aligned(slot_mapping, 8) ||
+        !aligned(positions, 4) || !aligned(status, 4))
+        return PA_ERR_INVALID_ARG;
+    const int64_t kv_row = (int64_t)num_kv_heads * head_dim, q_row = (int64_t)num_heads * head_dim;
+    const int64_t vec = 16 / eb;
+    // one row has no stride to check
+    if (num_tokens > 1 && ((num_heads && (query_stride < q_row || query_stride % vec)) || key_stride < kv_row ||
+                           key_stride % vec || value_stride < kv_row || value_stride % vec))
+        return PA_ERR_INVALID_ARG;
+    if (num_heads && num_tokens > 1 && query_out == query && query_stride != q_row) return PA_ERR_INVALID_ARG;
+    if ((int64_t)num_blocks * block_size > INT32_MAX) return PA_ERR_INVALID_ARG;
+    pa::RopeAxesArgs a{query_out,    query,        key,          value,     key_cache,  value_cache,
+                       slot_mapping, positions,    num_tokens,   num_heads, num_kv_heads, head_dim,
+                       query_stride, key_stride,   value_stride, block_size, num_blocks, kv_dtype,
+                       *rope,        status,       reinterpret_cast<cudaStream_t>(stream)};
+    return pa::launch_reshape_and_cache_rope_axes(a);
+}
+
 }  // extern "C"

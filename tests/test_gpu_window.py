@@ -1,0 +1,352 @@
+"""Windowed decode and prefill on the GPU against the 64-bit reference: every type, head
+layout and block size, windows and sinks of all proportions, contexts around their borders,
+pools that are NaN wherever no row looks, and the calls' conduct (streams, capture, bad
+tables, rows that must stay as they were)."""
+import numpy as np
+import pytest
+import torch
+
+from window_cases import assert_close, bound, make_case, reference
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+NAMES = {BF16: "bf16", FP16: "fp16", FP32: "fp32"}
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(cuda_ok):
+    yield
+
+
+def decode(case, out_dtype=FP32, status=None, out=None, t=None, **kw):
+    import paged_kv_attention_write_gb300 as pa
+    t = t or case.cuda()
+    out = torch.full(tuple(case.query.shape), 7.0, dtype=out_dtype, device="cuda") if out is None else out
+    pa.pa_decode_window(out, t["query"], t["key_cache"], t["value_cache"], t["tables"], t["ctx"], case.max_ctx,
+                        case.window, case.sinks, case.scale, status=status, **kw)
+    return out
+
+
+def prefill(case, out_dtype=FP32, status=None, out=None, t=None, **kw):
+    import paged_kv_attention_write_gb300 as pa
+    t = t or case.cuda()
+    out = torch.full(tuple(case.query.shape), 7.0, dtype=out_dtype, device="cuda") if out is None else out
+    pa.pa_prefill_window(out, t["query"], t["starts"], case.max_query, t["key_cache"], t["value_cache"], t["tables"],
+                         t["ctx"], case.max_ctx, case.window, case.sinks, case.scale, status=status, **kw)
+    return out
+
+
+def check(run, case, out_dtype=FP32, rounded=False):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = run(case, out_dtype, status)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    assert_close(out, case, out_dtype, rounded)
+
+
+# ------------------------------------------------------------------------------ decode
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 2), (8, 4), (1, 8), (16, 1), (2, 8), (4, 4)])
+@pytest.mark.parametrize("D,bs", [(64, 8), (64, 32), (128, 16), (128, 32)])
+def test_decode_heads_and_types(dtype, Hkv, G, D, bs):
+    case = make_case(dtype, Hkv * G, Hkv, D, bs, [0, 1, 2, 31, 32, 33, 100, 257, 999], 64, 5, seed=Hkv * 10 + G)
+    check(decode, case, FP32)
+    check(decode, case, dtype)
+
+
+@pytest.mark.parametrize("window", [1, 7, 8, 9, 64, 100, 513, 1 << 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("sinks", [0, 1, 4, 13, 32, 200, 2 ** 31 - 1])
+def test_decode_windows_and_sinks(window, sinks):
+    ctx = [0, 1, 7, 8, 9, 13, 63, 64, 65, 99, 100, 101, 104, 105, 113, 114, 200, 201, 300, 513, 514, 700]
+    check(decode, make_case(BF16, 8, 2, 64, 8, ctx, window, sinks, seed=window % 97 + sinks % 89), FP32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("S,window,D", [(1, 4096, 128), (1, 20000, 128), (2, 1000, 64), (33, 700, 128), (200, 300, 64)])
+def test_decode_long_contexts_and_batches(dtype, S, window, D):
+    rng = np.random.default_rng(S + window)
+    ctx = [int(c) for c in rng.integers(0, window + 3000, S)]
+    check(decode, make_case(dtype, 8, 2, D, 32, ctx, window, 4, seed=S), FP32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+def test_decode_large_scores_and_ties(dtype):
+    # keys that dwarf the others, all keys alike, and a sink that takes nearly all of the weight
+    case = make_case(dtype, 8, 2, 64, 16, [50, 300, 301], 40, 3, seed=5)
+    case.query *= 8
+    case.key_cache[case.tables[1, 0].long(), 0] *= 6
+    case.key_cache[case.tables[2, 17].long()] = case.key_cache[case.tables[2, 17].long(), :1]
+    t = case.cuda()
+    out = decode(case, FP32, t=t)
+    ref, mag = reference(case)
+    # |q| is eight times and one key six times larger than bound() assumes
+    e = 48 * bound(case, ref, mag, FP32, False)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= e).all()
+
+
+def test_decode_matches_plain_decode_when_the_window_is_open():
+    import paged_kv_attention_write_gb300 as pa
+    case = make_case(BF16, 32, 8, 128, 16, [1, 40, 333, 1025], 1 << 20, 0, seed=9)
+    t = case.cuda()
+    a = decode(case, FP32, t=t)
+    b = torch.empty_like(a)
+    ws = torch.empty(pa.pa_decode_workspace_size(4, 32, 8, 128, 1025), dtype=torch.uint8, device="cuda")
+    pa.pa_decode(b, t["query"], t["key_cache"], t["value_cache"], t["tables"], t["ctx"], 1025, case.scale, workspace=ws)
+    ref, mag = reference(case)
+    assert ((a - b).abs().double().cpu().numpy() <= 2 * bound(case, ref, mag, FP32, False)).all()
+
+
+def test_decode_is_repeatable_and_leaves_what_it_should_not_write():
+    case = make_case(BF16, 16, 4, 128, 16, [700, 0, 31, 1500], 256, 4, seed=2)
+    t = case.cuda()
+    before = {k: v.clone() for k, v in t.items()}
+    big = torch.full((9, 16, 128), 3.0, device="cuda")
+    out = decode(case, out=big[2:6], t=t).clone()
+    again = decode(case, t=t)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)
+    assert (big[:2] == 3).all() and (big[6:] == 3).all()
+    for k in t:
+        assert torch.equal(t[k].view(torch.uint8), before[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+def test_decode_reports_bad_blocks_and_contexts(dtype):
+    case = make_case(dtype, 8, 2, 64, 8, [500, 300, 40, 600], 100, 4, seed=3)
+    t = case.cuda()
+    good = decode(case, t=t)
+    t["tables"][0, 55] = case.key_cache.shape[0]      # a block of the window
+    t["tables"][3, 0] = -5                            # the sinks' block
+    t["tables"][1, 10] = 1 << 30                      # behind the window: not read
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = decode(case, t=t, status=status)
+    assert status.item() == 2
+    assert torch.equal(out[1:3], good[1:3])
+    # contexts out of range are clamped and reported
+    for bad, want in ((-7, 0), (2 ** 31 - 1, 600)):
+        t = case.cuda()
+        t["ctx"][3] = bad
+        status.zero_()
+        out = decode(case, t=t, status=status)
+        assert status.item() == 4
+        assert torch.equal(out[3], good[3] if want else torch.zeros_like(out[3]))
+        assert torch.equal(out[:3], good[:3])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+def test_decode_past_32_bits(dtype):
+    # positions up to 2^31 - 1 (the pages between the sinks and the window are not mapped)
+    width = (2 ** 31 - 1) // 32
+    top = width * 32
+    case = make_case(dtype, 4, 2, 64, 32, [9, 500], 100, 40, seed=4)
+    for ctx in (top, top - 31, top - 131):
+        far = make_case(dtype, 4, 2, 64, 32, [ctx % 32 + 32 * 40, 77], 100, 40, seed=4)
+        shift = ctx - int(far.ctx[0])
+        tables = torch.full((2, width), -1, dtype=torch.int32, device="cuda")
+        tables[1, :3] = far.tables[1, :3].cuda()
+        tables[0, :2] = far.tables[0, :2].cuda()
+        n = far.tables.shape[1]
+        tables[0, shift // 32 + 30: shift // 32 + n] = far.tables[0, 30:].cuda()
+        t = far.cuda()
+        t["tables"], t["ctx"] = tables, torch.tensor([ctx, 77], dtype=torch.int32, device="cuda")
+        import paged_kv_attention_write_gb300 as pa
+        out = torch.empty((2, 4, 64), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        pa.pa_decode_window(out, t["query"], t["key_cache"], t["value_cache"], tables, t["ctx"], ctx, 100, 40, far.scale,
+                            status=status)
+        assert status.item() == 0
+        assert_close(out, far, FP32, False)
+        if dtype == BF16:
+            q = t["query"]
+            starts = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+            pa.pa_prefill_window(out, q, starts, 1, t["key_cache"], t["value_cache"], tables, t["ctx"], ctx, 100, 40,
+                                 far.scale, status=status)
+            assert status.item() == 0
+            assert_close(out, far, FP32, True)
+    del case
+
+
+def test_decode_a_pool_past_32_bits():
+    # 6 GB of keys: element offsets of the last blocks pass 2^31
+    Hkv, D, bs, NB = 8, 128, 32, 98304
+    kc = torch.zeros((NB, bs, Hkv, D), dtype=BF16, device="cuda")
+    vc = torch.zeros_like(kc)
+    case = make_case(BF16, 16, Hkv, D, bs, [200, 90], 64, 4, chunks=[1, 1], seed=11)
+    used = sorted(set(case.tables[case.tables >= 0].tolist()))
+    moved = {b: NB - 1 - i * 11 for i, b in enumerate(used)}
+    for b, to in moved.items():
+        kc[to], vc[to] = case.key_cache[b].cuda(), case.value_cache[b].cuda()
+    t = case.cuda()
+    t["key_cache"], t["value_cache"] = kc, vc
+    t["tables"] = torch.tensor([[moved.get(b, -1) for b in row] for row in case.tables.tolist()], dtype=torch.int32,
+                               device="cuda")
+    assert_close(decode(case, t=t), case, FP32, False)
+    assert_close(prefill(case, t=t), case, FP32, True)
+
+
+# ------------------------------------------------------------------------------ prefill
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
+@pytest.mark.parametrize("Hkv,G", [(1, 1), (2, 2), (8, 4), (1, 8), (16, 1), (2, 8)])
+@pytest.mark.parametrize("D,bs", [(64, 8), (128, 16), (128, 32)])
+def test_prefill_heads_and_types(dtype, Hkv, G, D, bs):
+    case = make_case(dtype, Hkv * G, Hkv, D, bs, [1, 37, 300, 130, 513], 64, 5, chunks=[1, 37, 150, 2, 33],
+                     seed=Hkv * 10 + G)
+    check(prefill, case, FP32, True)
+    check(prefill, case, dtype, True)
+
+
+@pytest.mark.parametrize("window", [1, 7, 32, 100, 127, 128, 129, 500, 1 << 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("sinks", [0, 1, 4, 13, 32, 129, 300, 2 ** 31 - 1])
+def test_prefill_windows_and_sinks(window, sinks):
+    case = make_case(BF16, 8, 2, 64, 16, [0, 1, 140, 600, 333, 900], window, sinks, chunks=[0, 1, 140, 129, 64, 257],
+                     seed=window % 97 + sinks % 89)
+    check(prefill, case, FP32, True)
+
+
+@pytest.mark.parametrize("dtype,D", [(BF16, 128), (FP16, 64)])
+def test_prefill_many_ragged_chunks(dtype, D):
+    rng = np.random.default_rng(6)
+    chunks = [int(x) for x in rng.integers(0, 200, 40)]
+    ctx = [n + int(x) for n, x in zip(chunks, rng.integers(0, 1500, 40))]
+    check(prefill, make_case(dtype, 8, 2, D, 8, ctx, 333, 7, chunks=chunks, seed=7), dtype, True)
+
+
+def test_prefill_reports_bad_chunks_and_blocks():
+    case = make_case(BF16, 8, 2, 64, 8, [200, 300, 150], 60, 4, chunks=[40, 50, 60], seed=8)
+    t = case.cuda()
+    good = prefill(case, t=t)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    t["ctx"][1] = 49                                   # shorter than its chunk
+    out = prefill(case, t=t, status=status)
+    assert status.item() == 8
+    assert torch.equal(out[:40], good[:40]) and torch.equal(out[90:], good[90:]) and (out[40:90] == 7).all()
+    t = case.cuda()
+    t["tables"][0, 3] = 10 ** 6                        # behind the window: not read
+    t["tables"][2, 17] = 10 ** 6                       # seen
+    status.zero_()
+    out = prefill(case, t=t, status=status)
+    assert status.item() == 2
+    assert torch.equal(out[:90], good[:90])
+
+
+def test_prefill_rows_behind_the_last_chunk_stay():
+    case = make_case(BF16, 8, 2, 128, 16, [200, 130], 64, 4, chunks=[70, 33], seed=12)
+    t = case.cuda()
+    t["query"] = torch.cat([t["query"], torch.full((20, 8, 128), float("nan"), dtype=BF16, device="cuda")])
+    out = torch.full((123, 8, 128), 5.0, dtype=BF16, device="cuda")
+    prefill(case, t=t, out=out)
+    assert_close(out[:103], case, BF16, True)
+    assert (out[103:] == 5).all()
+
+
+# ------------------------------------------------------------------------------ conduct
+
+@pytest.mark.parametrize("run,rounded,chunks", [(decode, False, None), (prefill, True, [60, 1, 33])])
+def test_streams_and_graphs(run, rounded, chunks):
+    a = make_case(BF16, 8, 2, 128, 16, [300, 41, 999], 128, 4, chunks=chunks, seed=20)
+    b = make_case(BF16, 8, 2, 128, 16, [77, 500, 64], 128, 4, chunks=chunks, seed=21)
+    ta, tb = a.cuda(), b.cuda()
+    want_a, want_b = run(a, t=ta), run(b, t=tb)       # also the eager first call
+    torch.cuda.synchronize()
+    # two streams at once
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    oa, ob = torch.empty_like(want_a), torch.empty_like(want_b)
+    for _ in range(20):
+        run(a, out=oa, t=ta, stream=s1)
+        with torch.cuda.stream(s2):
+            run(b, out=ob, t=tb)
+    torch.cuda.synchronize()
+    assert torch.equal(oa, want_a) and torch.equal(ob, want_b)
+    # two captured calls, replayed in turn and over new inputs
+    graphs = []
+    for case, t, o in ((a, ta, oa), (b, tb, ob)):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run(case, out=o, t=t)
+        graphs.append(g)
+    oa.zero_()
+    ob.zero_()
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(oa, want_a) and torch.equal(ob, want_b)
+    ta["query"].copy_(ta["query"].flip(0))
+    fresh = run(a, t=ta)
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(oa, fresh)
+    assert_close(want_a, a, FP32, rounded)
+
+
+@pytest.mark.parametrize("sections,halves", [([16, 24, 24], True), ([20, 22, 22], False)])
+def test_a_stream_of_steps(sections, halves):
+    """Chunks, then single tokens, of two sequences through rotation, write and attention, with
+    the pages behind the window handed back and reused as the stream goes on."""
+    import paged_kv_attention_write_gb300 as pa
+    from oracle import rope as ref_rope
+    from oracle import window as ref_window
+    rng = np.random.default_rng(30)
+    Hq, Hkv, D, bs, window, sinks, NB, dt = 8, 2, 128, 8, 50, 4, 40, BF16
+    freqs = ref_rope.yarn_freqs(D, 1e4)
+    axes = ref_rope.pair_axes(D, sections)
+    rope = pa.RopeAxes(torch.from_numpy(freqs).cuda(), torch.from_numpy(axes).cuda(), D, 3, halves=halves)
+    kc = torch.full((NB, bs, Hkv, D), float("nan"), dtype=dt, device="cuda")
+    vc = kc.clone()
+    free, tables, S, width = list(range(NB)), None, 2, 64
+    tables = np.full((S, width), -1, dtype=np.int32)
+    length, keys, values = [0, 0], [np.zeros((0, Hkv, D))] * 2, [np.zeros((0, Hkv, D))] * 2
+    for step in [(30, 41), (64, 7), (1, 55)] + [(1, 1)] * 25:
+        qs, ks, vs, pos, slots = [], [], [], [], []
+        for s, n in enumerate(step):
+            lo = max(0, length[s] - window + 1)         # first key the step's first row sees
+            for b in range(width):                      # hand back the pages behind the window
+                if tables[s, b] >= 0 and b * bs >= sinks and (b + 1) * bs <= lo:
+                    kc[tables[s, b]] = vc[tables[s, b]] = float("nan")
+                    free.append(int(tables[s, b]))
+                    tables[s, b] = -1
+            at = np.arange(length[s], length[s] + n)
+            for b in np.unique(at // bs):
+                if tables[s, b] < 0:
+                    tables[s, b] = free.pop(0)
+            q, k, v = (torch.from_numpy(rng.standard_normal((n, h, D)).astype(np.float32)).to(dt) for h in (Hq, Hkv, Hkv))
+            p = np.stack([at, at // 5 + 100 * s, at % 7 + 3]).astype(np.int32)
+            keys[s] = np.concatenate([keys[s], ref_rope.apply_rope_axes(k.double().numpy(), p, freqs, axes, halves)])
+            values[s] = np.concatenate([values[s], v.double().numpy()])
+            length[s] += n
+            qs.append(q), ks.append(k), vs.append(v), pos.append(p)
+            slots.append(tables[s, at // bs].astype(np.int64) * bs + at % bs)
+        q, k, v = (torch.cat(x).cuda() for x in (qs, ks, vs))
+        p = np.concatenate(pos, 1)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        qr = torch.empty_like(q)
+        pa.pa_reshape_and_cache_rope_axes(qr, q, k, v, kc, vc, torch.from_numpy(np.concatenate(slots)).cuda(),
+                                          torch.from_numpy(p).cuda(), rope, status=status)
+        bt = torch.from_numpy(tables).cuda()
+        ctx = torch.tensor(length, dtype=torch.int32, device="cuda")
+        out = torch.empty((q.shape[0], Hq, D), device="cuda")
+        starts = np.concatenate([[0], np.cumsum(step)]).astype(np.int32)
+        if step == (1, 1):
+            pa.pa_decode_window(out, qr, kc, vc, bt, ctx, max(length), window, sinks, D ** -0.5, status=status)
+        else:
+            pa.pa_prefill_window(out, qr, torch.from_numpy(starts).cuda(), max(step), kc, vc, bt, ctx, max(length),
+                                 window, sinks, D ** -0.5, status=status)
+        assert status.item() == 0
+        q64 = ref_rope.apply_rope_axes(q.cpu().double().numpy(), p, freqs, axes, halves)
+        for s in range(S):
+            b, e = starts[s], starts[s + 1]
+            for r in range(b, e, max(1, (e - b) // 6)):
+                j = ref_window.visible(length[s] - (e - b) + (r - b), window, sinks)
+                for h in range(Hq):
+                    x = keys[s][j, h // 4] @ q64[r, h] * D ** -0.5
+                    w = np.exp(x - x.max())
+                    want = w @ values[s][j, h // 4] / w.sum()
+                    mag = w @ np.abs(values[s][j, h // 4]) / w.sum()
+                    # rotated queries and keys are rounded to bf16 (half a step, 2^-8, of each
+                    # element; independent signs, so a score moves by about 2^-8 |x| spread over
+                    # sqrt(2 D) products of size 1: under 6 deviations), weights once more
+                    e_score = 6 * 2.0 ** -8 * np.sqrt(2 * D) * D ** -0.5
+                    assert (np.abs(out[r, h].double().cpu().numpy() - want) <= 2 * (e_score + 2.0 ** -8) * mag).all()
