@@ -181,6 +181,42 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), std::atomic<int> *ready, d
     }
 }
 
+// launch_pdl_smem of a grid of clusters of `cluster` CTAs along x.
+template <class... KArgs, class... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), std::atomic<int> *ready, dim3 grid, dim3 block, size_t smem,
+                               int cluster, cudaStream_t stream, const Args &...args) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int> *flag = (dev >= 0 && dev < kMaxDevices) ? &ready[dev] : nullptr;
+    for (int attempt = 0;; ++attempt) {
+        const bool was_set = flag && flag->load(std::memory_order_acquire);
+        if (!was_set) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            if (flag) flag->store(1, std::memory_order_release);
+        }
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = cluster;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, kernel, args...);
+        if (e == cudaSuccess) e = cudaGetLastError();
+        if (e == cudaSuccess || !was_set || attempt > 0) return e;
+        flag->store(0, std::memory_order_release);
+    }
+}
+
 }  // namespace pa
 
 // ---------------------------------------------------------------- internal launchers

@@ -194,12 +194,6 @@ WindowParams params(const A &a) {
 
 }  // namespace
 
-int launch_decode_window(const DecodeArgs &a) {
-    WindowParams p = params(a);
-    p.num_tokens = a.num_seqs;
-    return dispatch(p, a.kv_dtype, a.head_dim, a.stream);
-}
-
 int launch_prefill_window(const PrefillArgs &a) {
     WindowParams p = params(a);
     p.num_tokens = a.num_tokens;
