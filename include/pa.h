@@ -339,7 +339,7 @@ int pa_decode_rope(void *out, pa_dtype out_dtype, const void *query, const void 
  *    anything (-1, say).  What the cache holds in slots that no row of the sequence sees is
  *    never used, not even NaN;
  *  - there is no workspace: the pieces of a split context are merged inside the launch.
- * window < 1 or num_sinks < 0 returns PA_ERR_INVALID_ARG.
+ * window < 1, num_sinks < 0 or scale <= 0 returns PA_ERR_INVALID_ARG.
  */
 
 /*
@@ -347,8 +347,9 @@ int pa_decode_rope(void *out, pa_dtype out_dtype, const void *query, const void 
  * context_lens[s] - 1) over the window and the sinks.  Arguments as for pa_decode; F32, F16
  * and BF16 caches.  A sequence with context length 0 gets an all-zero row; a negative
  * context, or one past max_context_len or the block table, is reported and clamped, as in
- * pa_decode.  fp32 accumulation; a row does not depend on the rest of the batch while the
- * batch size stays the same.
+ * pa_decode.  fp32 accumulation of fp32-accurate softmax weights for every
+ * cache type.  The split of a row depends on the call's sizes (num_seqs, max_context_len,
+ * window, num_sinks, heads) alone, not on the other rows' contents.
  */
 int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const void *key_cache,
                      const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,

@@ -661,13 +661,18 @@ int launch_decode_window(const DecodeArgs &a) {
                            : make_kv_block_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 8);
         if (rc != PA_OK) return rc;
     }
-    // The cluster size: CTAs for four per SM, but none with less than one stage of keys.
+    // The cluster size: the CTAs of one full wave, but none with less than one stage of keys.
+    // A CTA past the first wave costs more than its shorter run of keys gives back, and
+    // clusters start slowly: 256 (sequence, kv head) pairs of 1028 keys took 23, 29, 40 and
+    // 61 us in clusters of 1, 2, 4 and 8; 61 pairs of 790 keys 11.8, 8.6, 7.0 and 11.0 us;
+    // 8 pairs of 516 keys 11.1, 8.2, 6.5 and 5.9 us (bf16).
     const int sms = std::max(1, device_sm_count());
+    const int64_t slots = (int64_t)sms * (a.kv_dtype == PA_F32 ? 1 : 2);  // resident CTAs
     const int64_t most = std::min<int64_t>(a.max_context_len, (int64_t)a.window + a.num_sinks);  // keys of a row
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
     const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads;
     int cluster = 1;
-    while (cluster < 8 && pairs * cluster < 4 * sms && most > stage_keys * cluster) cluster *= 2;
+    while (cluster < 8 && pairs * cluster * 2 <= slots && most > stage_keys * cluster) cluster *= 2;
     switch (a.kv_dtype) {
         case PA_F32:
             return a.head_dim == 64 ? launch_f32<64>(p, cluster, a.num_seqs, km, vm, a.stream)

@@ -256,7 +256,7 @@ int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const voi
                              num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                              kv_dtype);
     if (rc != PA_OK) return rc;
-    if (window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (window < 1 || num_sinks < 0 || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0) return PA_OK;
     if (!aligned(status, 4)) return PA_ERR_INVALID_ARG;
     pa::DecodeArgs a{out,          out_dtype,      query,     key_cache,    value_cache,
@@ -282,7 +282,8 @@ int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
                              kv_dtype);
     if (rc != PA_OK) return rc;
     if (kv_dtype == PA_F32) return PA_ERR_UNSUPPORTED;
-    if (num_tokens < 0 || max_query_len < 0 || window < 1 || num_sinks < 0) return PA_ERR_INVALID_ARG;
+    if (num_tokens < 0 || max_query_len < 0 || window < 1 || num_sinks < 0 || !(scale > 0.f))
+        return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
     if (!query_start_loc || !aligned(query_start_loc, 4) || !aligned(status, 4))
         return PA_ERR_INVALID_ARG;

@@ -101,7 +101,7 @@ def _decode(lib, **over):
     (dict(window=0), -1), (dict(window=-3), -1), (dict(sinks=-1), -1), (dict(D=96), -2), (dict(bs=64), -2),
     (dict(Hq=24), -2), (dict(Hq=30), -1), (dict(kvdt=7), -1), (dict(out_dtype=9), -1), (dict(S=-1), -1),
     (dict(S=65536), -1), (dict(query=None), -1), (dict(out=None), -1), (dict(kc=FAKE + 4), -1), (dict(out=FAKE + 2), -1),
-    (dict(cl=FAKE + 1), -1), (dict(status=FAKE + 2), -1), (dict(scale=float("inf")), -1), (dict(maxctx=-5), -1),
+    (dict(cl=FAKE + 1), -1), (dict(status=FAKE + 2), -1), (dict(scale=float("inf")), -1), (dict(scale=0.0), -1), (dict(scale=-0.1), -1), (dict(maxctx=-5), -1),
     (dict(mbps=1 << 27), -1), (dict(NB=1 << 27), -1),
 ])
 def test_decode_window_refusals(lib, over, code):
@@ -125,7 +125,7 @@ def _prefill(lib, **over):
 
 
 @pytest.mark.parametrize("over,code", [
-    (dict(window=0), -1), (dict(sinks=-1), -1), (dict(kvdt=0), -2), (dict(D=96), -2), (dict(qsl=None), -1),
+    (dict(window=0), -1), (dict(sinks=-1), -1), (dict(scale=-1.0), -1), (dict(kvdt=0), -2), (dict(D=96), -2), (dict(qsl=None), -1),
     (dict(qsl=FAKE + 2), -1), (dict(T=-1), -1), (dict(mq=-1), -1), (dict(query=FAKE + 8), -1), (dict(Hkv=6, Hq=12), -2),
 ])
 def test_prefill_window_refusals(lib, over, code):
