@@ -272,67 +272,77 @@ def pa_decode_rope(out, query, key_cache, value_cache, block_tables, context_len
 
 # ----------------------------------------------------------------------------- sliding window
 
-def _require(ok: bool, what: str, why: str) -> None:
-    if not ok:
-        raise PAError(-1, f"{what}: {why}")
+def _refuse(what: str, why: str) -> None:
+    raise PAError(-1, f"{what}: {why}")
 
 
-def _run_on(dev: torch.device, stream, call):
-    """``call(stream handle)`` with the tensors' device current (a stream given must be of it)."""
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+def _call(dev: torch.device, stream, name, *args) -> None:
+    """Call a C entry point, stream last, with the tensors' device current (a stream given must
+    be of it).  Without one: torch's current stream of that device."""
+    f = getattr(_lib, name)
+    i = dev.index
+    if i == torch._C._cuda_getDevice():
+        code = f(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            code = f(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream))
+    if code != 0:
+        raise PAError(code, name)
 
 
-def _check_window(what, out, query, key_cache, value_cache, block_tables, ints, status) -> None:
-    """Shapes, types, layout and device of the windowed calls' tensors (``ints``: int32 vectors)."""
-    _require(query.dim() == 3 and key_cache.dim() == 4 and block_tables.dim() == 2, what,
-             "query is [T][Hq][D], a cache [NB][bs][Hkv][D], block_tables [S][max_blocks]")
-    _require(out.shape == query.shape and key_cache.shape == value_cache.shape and query.shape[2] == key_cache.shape[3],
-             what, "out is shaped as query, value_cache as key_cache, head dims are equal")
-    _require(query.dtype == key_cache.dtype == value_cache.dtype, what, "query and caches share one dtype")
-    _require(block_tables.dtype == torch.int32 and all(t.dtype == torch.int32 and t.dim() == 1 for t in ints) and
-             (status is None or status.dtype == torch.int32), what,
-             "tables, lengths, starts and status are int32")
+def _check_window(what, out, query, key_cache, value_cache, tables, lens, starts, status) -> torch.device:
+    """Shapes, types, layout and device of the windowed calls' tensors; returns the device."""
+    if query.dim() != 3 or key_cache.dim() != 4 or tables.dim() != 2 or lens.dim() != 1:
+        _refuse(what, "query is [T][Hq][D], a cache [NB][bs][Hkv][D], block_tables [S][max_blocks], lengths [S]")
+    if out.shape != query.shape or key_cache.shape != value_cache.shape or query.shape[2] != key_cache.shape[3]:
+        _refuse(what, "out is shaped as query, value_cache as key_cache, head dims are equal")
+    dt = query.dtype
+    if key_cache.dtype != dt or value_cache.dtype != dt:
+        _refuse(what, "query and caches share one dtype")
+    i32 = torch.int32
+    if tables.dtype != i32 or lens.dtype != i32 or (starts is not None and starts.dtype != i32) or (
+            status is not None and status.dtype != i32):
+        _refuse(what, "tables, lengths, starts and status are int32")
+    rows = lens.shape[0]
+    if tables.shape[0] != rows or (query.shape[0] != rows if starts is None else starts.shape != (rows + 1,)):
+        _refuse(what, "one table row and length per sequence, one query row each or S + 1 row starts")
+    if not (out.is_contiguous() and query.is_contiguous() and key_cache.is_contiguous() and
+            value_cache.is_contiguous() and tables.is_contiguous() and lens.is_contiguous() and
+            (starts is None or starts.is_contiguous())):
+        _refuse(what, "tensors must be contiguous")
     dev = query.device
-    ts = (out, query, key_cache, value_cache, block_tables, *ints) if status is None else (
-        out, query, key_cache, value_cache, block_tables, status, *ints)
-    _require(all(t.is_contiguous() for t in ts), what, "tensors must be contiguous")
-    _require(dev.type == "cuda" and all(t.device == dev for t in ts), what, "tensors must be on one CUDA device")
+    if dev.type != "cuda" or not (out.device == dev == key_cache.device == value_cache.device == tables.device ==
+                                  lens.device) or (starts is not None and starts.device != dev) or (
+            status is not None and status.device != dev):
+        _refuse(what, "tensors must be on one CUDA device")
+    return dev
 
 
 def pa_decode_window(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len: int,
                      window: int, num_sinks: int, scale: float, *, status=None, stream=None) -> None:
     """pa_decode over the newest ``window`` keys and the first ``num_sinks`` of each sequence.
     No workspace; table entries of blocks that no key is seen in are not read."""
-    _check_window("pa_decode_window", out, query, key_cache, value_cache, block_tables, (context_lens,), status)
+    dev = _check_window("pa_decode_window", out, query, key_cache, value_cache, block_tables, context_lens, None, status)
     S, Hq, D = query.shape
     NB, bs, Hkv, _ = key_cache.shape
-    _require(block_tables.shape[0] == S == context_lens.shape[0], "pa_decode_window",
-             "one query row, table row and context length per sequence")
-    _check(_run_on(query.device, stream, lambda st: _lib.pa_decode_window(
-        _ptr(out), _dt(out), _ptr(query), _ptr(key_cache), _ptr(value_cache), _ptr(block_tables),
-        block_tables.shape[1], _ptr(context_lens), int(max_context_len), int(window), int(num_sinks), S, Hq, Hkv, D,
-        bs, NB, float(scale), _dt(key_cache), _ptr(status), st)), "pa_decode_window")
+    _call(dev, stream, "pa_decode_window", out.data_ptr(), _dt(out), query.data_ptr(), key_cache.data_ptr(),
+          value_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+          int(max_context_len), int(window), int(num_sinks), S, Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache),
+          _ptr(status))
 
 
 def pa_prefill_window(out, query, query_start_loc, max_query_len: int, key_cache, value_cache, block_tables,
                       context_lens, max_context_len: int, window: int, num_sinks: int, scale: float, *, status=None,
                       stream=None) -> None:
     """pa_prefill_chunk over the newest ``window`` keys before each row and the first ``num_sinks``."""
-    _check_window("pa_prefill_window", out, query, key_cache, value_cache, block_tables,
-                  (context_lens, query_start_loc), status)
+    dev = _check_window("pa_prefill_window", out, query, key_cache, value_cache, block_tables, context_lens,
+                        query_start_loc, status)
     Tq, Hq, D = query.shape
     NB, bs, Hkv, _ = key_cache.shape
-    S = context_lens.shape[0]
-    _require(block_tables.shape[0] == S and query_start_loc.shape[0] == S + 1, "pa_prefill_window",
-             "one table row per sequence, S + 1 row starts")
-    _check(_run_on(query.device, stream, lambda st: _lib.pa_prefill_window(
-        _ptr(out), _dt(out), _ptr(query), _ptr(query_start_loc), Tq, int(max_query_len), _ptr(key_cache),
-        _ptr(value_cache), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), int(max_context_len),
-        int(window), int(num_sinks), S, Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache), _ptr(status), st)),
-        "pa_prefill_window")
+    _call(dev, stream, "pa_prefill_window", out.data_ptr(), _dt(out), query.data_ptr(), query_start_loc.data_ptr(), Tq,
+          int(max_query_len), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+          block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), int(window), int(num_sinks),
+          context_lens.shape[0], Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache), _ptr(status))
 
 
 # ----------------------------------------------------------------------------- rotary axes
@@ -355,16 +365,16 @@ class RopeAxes:
 
     def __init__(self, freqs: torch.Tensor, pair_axis: torch.Tensor, rope_dim: int, num_axes: int,
                  halves: bool = False):
-        _require(freqs.dtype == torch.float32 and pair_axis.dtype == torch.int32 and freqs.is_contiguous() and
-                 pair_axis.is_contiguous() and 2 * freqs.numel() == rope_dim == 2 * pair_axis.numel() and
-                 freqs.device == pair_axis.device, "RopeAxes",
-                 "freqs is fp32 and pair_axis int32, both [rope_dim / 2], dense, on one device")
+        n = rope_dim // 2
+        if not (freqs.dtype == torch.float32 and pair_axis.dtype == torch.int32 and rope_dim % 2 == 0 and
+                freqs.shape == (n,) and pair_axis.shape == (n,) and freqs.is_contiguous() and
+                pair_axis.is_contiguous() and freqs.device == pair_axis.device):
+            _refuse("RopeAxes", "freqs is fp32 and pair_axis int32, both [rope_dim / 2], dense, on one device")
         self.freqs, self.pair_axis = freqs, pair_axis
         self.rope_dim, self.num_axes, self.halves = int(rope_dim), int(num_axes), bool(halves)
 
     def _c(self):
-        return _PaRopeAxes(self.freqs.data_ptr(), self.pair_axis.data_ptr(), self.rope_dim, self.num_axes,
-                           int(self.halves))
+        return _PaRopeAxes(self.freqs.data_ptr(), self.pair_axis.data_ptr(), self.rope_dim, self.num_axes, self.halves)
 
 
 def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
@@ -374,36 +384,43 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
     (int32 [num_axes][T]).  query, key and value may be slices of wider rows.  ``query`` and
     ``query_out`` None: keys and values only."""
     what = "pa_reshape_and_cache_rope_axes"
-    _require((query is None) == (query_out is None), what, "query and query_out go together")
-    _require(key.dim() == 3 and key.shape == value.shape and key_cache.dim() == 4 and
-             key_cache.shape == value_cache.shape and key.shape[1:] == key_cache.shape[2:], what,
-             "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
+    if (query is None) != (query_out is None):
+        _refuse(what, "query and query_out go together")
+    if key.dim() != 3 or key_cache.dim() != 4 or key.shape != value.shape or key_cache.shape != value_cache.shape or (
+            key.shape[1:] != key_cache.shape[2:]):
+        _refuse(what, "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
     T, Hkv, D = key.shape
     NB, bs = key_cache.shape[:2]
-    rows, dense = [key, value], [key_cache, value_cache, slot_mapping, positions]
-    Hq = 0
+    dt, dev = key.dtype, key.device
+    Hq = q_stride = 0
     if query is not None:
-        _require(query.dim() == 3 and query.shape == query_out.shape and query.shape[0] == T and query.shape[2] == D,
-                 what, "query and query_out are [T][Hq][D]")
+        if query.dim() != 3 or query.shape != query_out.shape or query.shape[0] != T or query.shape[2] != D:
+            _refuse(what, "query and query_out are [T][Hq][D]")
         Hq = query.shape[1]
-        rows.append(query)
-        dense.append(query_out)
-        _require(query_out.dtype == query.dtype == key.dtype, what, "query, keys and caches share one dtype")
-    if status is not None:
-        dense.append(status)
-    _require(key.dtype == value.dtype == key_cache.dtype == value_cache.dtype, what,
-             "query, keys, values and caches share one dtype")
-    _require(slot_mapping.dtype == torch.int64 and slot_mapping.shape == (T,) and positions.dtype == torch.int32 and
-             positions.shape == (rope.num_axes, T) and (status is None or status.dtype == torch.int32), what,
-             "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32")
-    _require(all(t.is_contiguous() for t in dense), what, "caches, query_out, slots and positions must be contiguous")
-    _require(T == 0 or all(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == D) for t in rows), what,
-             "a token's heads must be contiguous")
-    dev = key.device
-    _require(dev.type == "cuda" and rope.freqs.device == dev and all(t.device == dev for t in rows) and
-             all(t.device == dev for t in dense), what, "tensors must be on one CUDA device")
-    r = rope._c()
-    _check(_run_on(dev, stream, lambda st: _lib.pa_reshape_and_cache_rope_axes(
-        _ptr(query_out), _ptr(query), _ptr(key), _ptr(value), _ptr(key_cache), _ptr(value_cache),
-        _ptr(slot_mapping), _ptr(positions), T, Hq, Hkv, D, 0 if query is None else query.stride(0), key.stride(0),
-        value.stride(0), bs, NB, _dt(key_cache), ctypes.byref(r), _ptr(status), st)), what)
+        q_stride, q_head, q_one = query.stride()
+        if query.dtype != dt or query_out.dtype != dt:
+            _refuse(what, "query, keys, values and caches share one dtype")
+        if T and (q_one != 1 or (Hq > 1 and q_head != D)):
+            _refuse(what, "a token's heads must be contiguous")
+        if not query_out.is_contiguous():
+            _refuse(what, "caches, query_out, slots and positions must be contiguous")
+    if value.dtype != dt or key_cache.dtype != dt or value_cache.dtype != dt:
+        _refuse(what, "query, keys, values and caches share one dtype")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or positions.dtype != torch.int32 or (
+            positions.shape != (rope.num_axes, T)) or (status is not None and status.dtype != torch.int32):
+        _refuse(what, "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32")
+    if not (key_cache.is_contiguous() and value_cache.is_contiguous() and slot_mapping.is_contiguous() and
+            positions.is_contiguous()):
+        _refuse(what, "caches, query_out, slots and positions must be contiguous")
+    k_stride, k_head, k_one = key.stride()
+    v_stride, v_head, v_one = value.stride()
+    if T and (k_one != 1 or v_one != 1 or (Hkv > 1 and (k_head != D or v_head != D))):
+        _refuse(what, "a token's heads must be contiguous")
+    if dev.type != "cuda" or not (value.device == dev == key_cache.device == value_cache.device ==
+                                  slot_mapping.device == positions.device == rope.freqs.device) or (
+            query is not None and not (query.device == dev == query_out.device)) or (
+            status is not None and status.device != dev):
+        _refuse(what, "tensors must be on one CUDA device")
+    _call(dev, stream, what, _ptr(query_out), _ptr(query), key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
+          value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), T, Hq, Hkv, D, q_stride, k_stride,
+          v_stride, bs, NB, _dt(key_cache), ctypes.byref(rope._c()), _ptr(status))

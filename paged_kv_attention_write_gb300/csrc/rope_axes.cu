@@ -1,17 +1,214 @@
 // rope_axes.cu -- rotary positions with several axes, for a step's queries and keys, fused
 // with the cache write.
 //
-// Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i].  One CTA per token: the
-// (cos, sin) of its pairs go to shared memory once and serve all of its heads; the threads
-// then rotate the query and key elements pair by pair and copy the values.
-#include "common.cuh"
+// Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i]:
+// (x, y) -> (x cos - y sin, x sin + y cos).  Every element is read and written once, so the
+// kernel is bound by HBM; what it must avoid is waiting.  A CTA takes whole tokens: 64
+// threads at most compute the (cos, sin) of the token's pairs into shared memory while all
+// of them already have their first vectors in flight; a thread then keeps the pairs of one
+// place in the head in registers and applies them to the same place of every head it owns.
+#include <algorithm>
+
+#include "tma.cuh"  // device_sm_count
 
 namespace pa {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxPairs = 64;  // rope_dim <= head_dim <= 128
+constexpr int kAhead = 4;      // heads of a thread whose loads are in flight together
 
+// A 16-byte load that does not stay in L1 (queries may be rotated in place, so not through
+// the read-only path).
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ void set_word(uint4 &v, int i, uint32_t w) {
+    if (i == 0) v.x = w;
+    if (i == 1) v.y = w;
+    if (i == 2) v.z = w;
+    if (i == 3) v.w = w;
+}
+__device__ __forceinline__ float2 unpack(F16, uint32_t w) {
+    float2 f;
+    widen_pair_f16(w, f.x, f.y);
+    return f;
+}
+__device__ __forceinline__ float2 unpack(BF16, uint32_t w) {
+    float2 f;
+    widen_pair_bf16(w, f.x, f.y);
+    return f;
+}
+__device__ __forceinline__ uint32_t pack(F16, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t pack(BF16, float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 turn(float x, float y, float2 cs) {
+    return make_float2(x * cs.x - y * cs.y, x * cs.y + y * cs.x);
+}
+
+// The elements of a against those of b (halves pairing), all rotated.
+template <class T>
+__device__ __forceinline__ void rotate_across(T t, uint4 &a, uint4 &b, const float2 *cs) {
+    if constexpr (T::kPerVec == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 r = turn(__uint_as_float(word(a, i)), __uint_as_float(word(b, i)), cs[i]);
+            set_word(a, i, __float_as_uint(r.x));
+            set_word(b, i, __float_as_uint(r.y));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack(t, word(a, i)), y = unpack(t, word(b, i));
+            const float2 r0 = turn(x.x, y.x, cs[2 * i]), r1 = turn(x.y, y.y, cs[2 * i + 1]);
+            set_word(a, i, pack(t, r0.x, r1.x));
+            set_word(b, i, pack(t, r0.y, r1.y));
+        }
+    }
+}
+
+// The first `n` adjacent pairs of a vector; the others keep their bits.
+template <class T>
+__device__ __forceinline__ void rotate_adjacent(T t, uint4 &a, const float2 *cs, int n) {
+    if constexpr (T::kPerVec == 4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 r = turn(__uint_as_float(word(a, 2 * i)), __uint_as_float(word(a, 2 * i + 1)), cs[i]);
+            if (i < n) {
+                set_word(a, 2 * i, __float_as_uint(r.x));
+                set_word(a, 2 * i + 1, __float_as_uint(r.y));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack(t, word(a, i)), r = turn(x.x, x.y, cs[i]);
+            if (i < n) set_word(a, i, pack(t, r.x, r.y));
+        }
+    }
+}
+
+// (cos, sin) of the pairs i = threadIdx.x, + kThreads, .. of token t.
+__device__ __forceinline__ void angles(const RopeAxesArgs &p, int t, int half, float2 *cs) {
+    for (int i = threadIdx.x; i < half; i += kThreads) {
+        const int axis = p.rope.pair_axis[i];
+        const bool ok = axis >= 0 && axis < p.rope.num_axes;
+        if (!ok && t == 0) report(p.status, PA_DEVERR_AXIS);
+        cs[i] = ok ? rope_cos_sin(p.positions[(int64_t)axis * p.num_tokens + t], p.rope.freqs[i]) : make_float2(1.f, 0.f);
+    }
+}
+
+// One piece of a thread: vectors a and b (16 bytes each) of one head.
+template <class T, int D, bool HALVES>
+__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs p) {
+    using ST = typename T::storage;
+    constexpr int EPV = T::kPerVec, PER_HEAD = D / EPV / 2;  // threads per head, two vectors each
+    constexpr int STEP = kThreads / PER_HEAD;                // heads per pass of the CTA
+    constexpr int HP = EPV / 2;                              // adjacent pairs of a vector
+    __shared__ float2 cs_all[2][kMaxPairs];
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const int half = p.rope.rope_dim / 2, j = threadIdx.x % PER_HEAD, h0 = threadIdx.x / PER_HEAD;
+    const int Hq = p.num_heads, Hkv = p.num_kv_heads, heads = Hq + 2 * Hkv;
+    // this thread's two vectors of a head, and what turns them
+    int a, b, pa_ = 0, pb = 0, na = 0, nb = 0;
+    bool rotated;
+    if constexpr (HALVES) {
+        const int hv = half / EPV;
+        rotated = j < hv;
+        a = rotated ? j : 2 * j;
+        b = rotated ? j + hv : 2 * j + 1;
+        pa_ = j * EPV;
+    } else {
+        a = j;
+        b = j + PER_HEAD;
+        pa_ = a * HP;
+        pb = b * HP;
+        na = max(0, min(HP, half - pa_));
+        nb = max(0, min(HP, half - pb));
+        rotated = na > 0;
+    }
+    a *= EPV;
+    b *= EPV;
+    int buf = 0;
+    for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x, buf ^= 1) {
+        const int64_t slot = p.slot_mapping[t];
+        const bool write = slot >= 0 && slot < (int64_t)p.num_blocks * p.block_size;
+        if (slot >= 0 && !write && threadIdx.x == 0) report(p.status, PA_DEVERR_SLOT);
+        const int todo = write ? heads : Hq;
+        auto source = [&](int h) {
+            return h < Hq ? static_cast<const ST *>(p.query) + t * p.query_stride + h * D
+                   : h < Hq + Hkv ? static_cast<const ST *>(p.key) + t * p.key_stride + (h - Hq) * D
+                                  : static_cast<const ST *>(p.value) + t * p.value_stride + (h - Hq - Hkv) * D;
+        };
+        auto target = [&](int h) {
+            return h < Hq ? static_cast<ST *>(p.query_out) + ((int64_t)t * Hq + h) * D
+                   : h < Hq + Hkv ? static_cast<ST *>(p.key_cache) + (slot * Hkv + h - Hq) * D
+                                  : static_cast<ST *>(p.value_cache) + (slot * Hkv + h - Hq - Hkv) * D;
+        };
+        uint4 va[kAhead], vb[kAhead];
+        auto load = [&](int first) {
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = first + u * STEP;
+                if (h < todo) {
+                    const ST *src = source(h);
+                    va[u] = ld_once(src + a);
+                    vb[u] = ld_once(src + b);
+                }
+            }
+        };
+        load(h0);
+        float2 *cs = cs_all[buf];  // the other buffer may still be read by a slower warp
+        angles(p, t, half, cs);
+        __syncthreads();
+        float2 c[EPV];
+        if (rotated) {
+#pragma unroll
+            for (int e = 0; e < EPV; ++e) {
+                if constexpr (HALVES)
+                    c[e] = cs[pa_ + e];
+                else
+                    c[e] = e < HP ? (e < na ? cs[pa_ + e] : make_float2(1.f, 0.f))
+                                  : (e - HP < nb ? cs[pb + e - HP] : make_float2(1.f, 0.f));
+            }
+        }
+        for (int first = h0; first < todo; first += kAhead * STEP) {
+            if (first != h0) load(first);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int h = first + u * STEP;
+                if (h < todo) {
+                    if (rotated && h < Hq + Hkv) {
+                        if constexpr (HALVES) {
+                            rotate_across(T{}, va[u], vb[u], c);
+                        } else {
+                            rotate_adjacent(T{}, va[u], c, na);
+                            rotate_adjacent(T{}, vb[u], c + HP, nb);
+                        }
+                    }
+                    ST *dst = target(h);
+                    *reinterpret_cast<uint4 *>(dst + a) = va[u];
+                    *reinterpret_cast<uint4 *>(dst + b) = vb[u];
+                }
+            }
+        }
+    }
+}
+
+// The halves pairing of a width whose half is not a whole number of 16-byte vectors: element
+// by element, one CTA per token.
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -20,47 +217,33 @@ __device__ __forceinline__ void from_float(float v, __half &x) { x = __float2hal
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16 &x) { x = __float2bfloat16_rn(v); }
 
 template <class ST>
-__device__ void rotate_row(ST *dst, const ST *src, const float2 *cs, int heads, int D, int half, bool halves) {
+__device__ void rotate_elements(ST *dst, const ST *src, const float2 *cs, int heads, int D, int half) {
     for (int i = threadIdx.x; i < heads * (D / 2); i += kThreads) {
         const int h = i / (D / 2), pair = i % (D / 2);
-        int a, b;
+        const int a = h * D + (pair < half ? pair : 2 * pair), b = h * D + (pair < half ? pair + half : 2 * pair + 1);
+        const ST xs = src[a], ys = src[b];
         if (pair < half) {
-            a = halves ? pair : 2 * pair;
-            b = halves ? pair + half : 2 * pair + 1;
+            const float2 r = turn(to_float(xs), to_float(ys), cs[pair]);
+            from_float(r.x, dst[a]);
+            from_float(r.y, dst[b]);
         } else {
-            a = 2 * pair;
-            b = 2 * pair + 1;
-        }
-        const ST xs = src[h * D + a], ys = src[h * D + b];
-        if (pair < half) {
-            const float2 c = cs[pair];
-            const float x = to_float(xs), y = to_float(ys);
-            from_float(x * c.x - y * c.y, dst[h * D + a]);
-            from_float(x * c.y + y * c.x, dst[h * D + b]);
-        } else {
-            dst[h * D + a] = xs;
-            dst[h * D + b] = ys;
+            dst[a] = xs;
+            dst[b] = ys;
         }
     }
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs p) {
+__global__ void __launch_bounds__(kThreads) rope_axes_odd_halves_kernel(const RopeAxesArgs p) {
     using ST = typename T::storage;
     __shared__ float2 cs[kMaxPairs];
     pdl_wait_previous();
     pdl_launch_dependents();
     const int t = blockIdx.x, D = p.head_dim, half = p.rope.rope_dim / 2;
-    for (int i = threadIdx.x; i < half; i += kThreads) {
-        const int axis = p.rope.pair_axis[i];
-        const bool ok = axis >= 0 && axis < p.rope.num_axes;
-        if (!ok && t == 0) report(p.status, PA_DEVERR_AXIS);
-        cs[i] = ok ? rope_cos_sin(p.positions[(int64_t)axis * p.num_tokens + t], p.rope.freqs[i]) : make_float2(1.f, 0.f);
-    }
+    angles(p, t, half, cs);
     __syncthreads();
-    if (p.num_heads)
-        rotate_row(static_cast<ST *>(p.query_out) + (int64_t)t * p.num_heads * D,
-                   static_cast<const ST *>(p.query) + t * p.query_stride, cs, p.num_heads, D, half, p.rope.halves);
+    rotate_elements(static_cast<ST *>(p.query_out) + (int64_t)t * p.num_heads * D,
+                    static_cast<const ST *>(p.query) + t * p.query_stride, cs, p.num_heads, D, half);
     const int64_t slot = p.slot_mapping[t];
     if (slot < 0) return;
     if (slot >= (int64_t)p.num_blocks * p.block_size) {
@@ -68,10 +251,28 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs 
         return;
     }
     const int64_t row = slot * p.num_kv_heads * D;
-    rotate_row(static_cast<ST *>(p.key_cache) + row, static_cast<const ST *>(p.key) + t * p.key_stride, cs,
-               p.num_kv_heads, D, half, p.rope.halves);
+    rotate_elements(static_cast<ST *>(p.key_cache) + row, static_cast<const ST *>(p.key) + t * p.key_stride, cs,
+                    p.num_kv_heads, D, half);
     for (int i = threadIdx.x; i < p.num_kv_heads * D; i += kThreads)
         static_cast<ST *>(p.value_cache)[row + i] = static_cast<const ST *>(p.value)[t * p.value_stride + i];
+}
+
+template <class T, int D>
+cudaError_t launch_typed(const RopeAxesArgs &a) {
+    if (a.rope.halves && (a.rope.rope_dim / 2) % T::kPerVec != 0)
+        return launch_pdl(rope_axes_odd_halves_kernel<T>, dim3(a.num_tokens), dim3(kThreads), 0, a.stream, a);
+    // CTAs of equal numbers of tokens, in one wave of kPerSm CTAs per SM at most
+    constexpr int kPerSm = 12;
+    const int64_t slots = (int64_t)std::max(1, device_sm_count()) * kPerSm;
+    const int64_t each = (a.num_tokens + slots - 1) / slots;
+    const dim3 grid((unsigned)((a.num_tokens + each - 1) / each));
+    return a.rope.halves ? launch_pdl(rope_axes_kernel<T, D, true>, grid, dim3(kThreads), 0, a.stream, a)
+                         : launch_pdl(rope_axes_kernel<T, D, false>, grid, dim3(kThreads), 0, a.stream, a);
+}
+
+template <class T>
+cudaError_t launch_dim(const RopeAxesArgs &a) {
+    return a.head_dim == 64 ? launch_typed<T, 64>(a) : launch_typed<T, 128>(a);
 }
 
 }  // namespace
@@ -79,9 +280,9 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs 
 int launch_reshape_and_cache_rope_axes(const RopeAxesArgs &a) {
     cudaError_t e;
     switch (a.kv_dtype) {
-        case PA_F32: e = launch_pdl(rope_axes_kernel<F32>, dim3(a.num_tokens), dim3(kThreads), 0, a.stream, a); break;
-        case PA_F16: e = launch_pdl(rope_axes_kernel<F16>, dim3(a.num_tokens), dim3(kThreads), 0, a.stream, a); break;
-        case PA_BF16: e = launch_pdl(rope_axes_kernel<BF16>, dim3(a.num_tokens), dim3(kThreads), 0, a.stream, a); break;
+        case PA_F32: e = launch_dim<F32>(a); break;
+        case PA_F16: e = launch_dim<F16>(a); break;
+        case PA_BF16: e = launch_dim<BF16>(a); break;
         default: return PA_ERR_UNSUPPORTED;
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
