@@ -17,6 +17,7 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kMaxPairs = 64;  // rope_dim <= head_dim <= 128
 constexpr int kAhead = 4;      // heads of a thread whose loads are in flight together
+constexpr int kPerSm = 5;      // resident CTAs per SM
 
 // A 16-byte load that does not stay in L1 (queries may be rotated in place, so not through
 // the read-only path).
@@ -99,19 +100,26 @@ __device__ __forceinline__ void rotate_adjacent(T t, uint4 &a, const float2 *cs,
     }
 }
 
-// (cos, sin) of the pairs i = threadIdx.x, + kThreads, .. of token t.
-__device__ __forceinline__ void angles(const RopeAxesArgs &p, int t, int half, float2 *cs) {
-    for (int i = threadIdx.x; i < half; i += kThreads) {
-        const int axis = p.rope.pair_axis[i];
-        const bool ok = axis >= 0 && axis < p.rope.num_axes;
-        if (!ok && t == 0) report(p.status, PA_DEVERR_AXIS);
-        cs[i] = ok ? rope_cos_sin(p.positions[(int64_t)axis * p.num_tokens + t], p.rope.freqs[i]) : make_float2(1.f, 0.f);
+// The pair whose angle this thread computes for every token of its CTA (pair threadIdx.x; a
+// row has at most kMaxPairs).
+struct Pair {
+    const int32_t *positions;  // of its axis; null: no such pair, or a bad axis (not rotated)
+    float freq;
+    __device__ __forceinline__ explicit Pair(const RopeAxesArgs &p) : positions(nullptr), freq(0.f) {
+        if ((int)threadIdx.x >= p.rope.rope_dim / 2) return;
+        const int axis = p.rope.pair_axis[threadIdx.x];
+        freq = p.rope.freqs[threadIdx.x];
+        if (axis >= 0 && axis < p.rope.num_axes)
+            positions = p.positions + (int64_t)axis * p.num_tokens;
+        else if (blockIdx.x == 0)
+            report(p.status, PA_DEVERR_AXIS);
     }
-}
+    __device__ __forceinline__ int position(int t) const { return positions ? positions[t] : 0; }  // angle 0
+};
 
 // One piece of a thread: vectors a and b (16 bytes each) of one head.
 template <class T, int D, bool HALVES>
-__global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs p) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rope_axes_kernel(const RopeAxesArgs p) {
     using ST = typename T::storage;
     constexpr int EPV = T::kPerVec, PER_HEAD = D / EPV / 2;  // threads per head, two vectors each
     constexpr int STEP = kThreads / PER_HEAD;                // heads per pass of the CTA
@@ -141,12 +149,11 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs 
     }
     a *= EPV;
     b *= EPV;
+    const Pair pair(p);
     int buf = 0;
     for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x, buf ^= 1) {
         const int64_t slot = p.slot_mapping[t];
-        const bool write = slot >= 0 && slot < (int64_t)p.num_blocks * p.block_size;
-        if (slot >= 0 && !write && threadIdx.x == 0) report(p.status, PA_DEVERR_SLOT);
-        const int todo = write ? heads : Hq;
+        const int pos = pair.position(t);
         auto source = [&](int h) {
             return h < Hq ? static_cast<const ST *>(p.query) + t * p.query_stride + h * D
                    : h < Hq + Hkv ? static_cast<const ST *>(p.key) + t * p.key_stride + (h - Hq) * D
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs 
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int h = first + u * STEP;
-                if (h < todo) {
+                if (h < heads) {  // whatever the slot: the loads do not wait for it
                     const ST *src = source(h);
                     va[u] = ld_once(src + a);
                     vb[u] = ld_once(src + b);
@@ -171,8 +178,11 @@ __global__ void __launch_bounds__(kThreads) rope_axes_kernel(const RopeAxesArgs 
         };
         load(h0);
         float2 *cs = cs_all[buf];  // the other buffer may still be read by a slower warp
-        angles(p, t, half, cs);
+        if ((int)threadIdx.x < half) cs[threadIdx.x] = rope_cos_sin(pos, pair.freq);
         __syncthreads();
+        const bool write = slot >= 0 && slot < (int64_t)p.num_blocks * p.block_size;
+        if (slot >= 0 && !write && threadIdx.x == 0) report(p.status, PA_DEVERR_SLOT);
+        const int todo = write ? heads : Hq;
         float2 c[EPV];
         if (rotated) {
 #pragma unroll
@@ -240,7 +250,8 @@ __global__ void __launch_bounds__(kThreads) rope_axes_odd_halves_kernel(const Ro
     pdl_wait_previous();
     pdl_launch_dependents();
     const int t = blockIdx.x, D = p.head_dim, half = p.rope.rope_dim / 2;
-    angles(p, t, half, cs);
+    const Pair pair(p);
+    if ((int)threadIdx.x < half) cs[threadIdx.x] = rope_cos_sin(pair.position(t), pair.freq);
     __syncthreads();
     rotate_elements(static_cast<ST *>(p.query_out) + (int64_t)t * p.num_heads * D,
                     static_cast<const ST *>(p.query) + t * p.query_stride, cs, p.num_heads, D, half);
@@ -261,8 +272,7 @@ template <class T, int D>
 cudaError_t launch_typed(const RopeAxesArgs &a) {
     if (a.rope.halves && (a.rope.rope_dim / 2) % T::kPerVec != 0)
         return launch_pdl(rope_axes_odd_halves_kernel<T>, dim3(a.num_tokens), dim3(kThreads), 0, a.stream, a);
-    // CTAs of equal numbers of tokens, in one wave of kPerSm CTAs per SM at most
-    constexpr int kPerSm = 12;
+    // CTAs of equal numbers of tokens, in one wave
     const int64_t slots = (int64_t)std::max(1, device_sm_count()) * kPerSm;
     const int64_t each = (a.num_tokens + slots - 1) / slots;
     const dim3 grid((unsigned)((a.num_tokens + each - 1) / each));
