@@ -221,6 +221,12 @@ struct PfWindow {
     int lo, ns;          // first window key of the first row; sinks in front of it
     int sinks, shift;    // blocks of sinks; logical block of virtual block v >= sinks: v + shift
     int blocks;          // virtual blocks
+    int low_tiles;       // key tiles that hold sinks or keys behind some row's window: the first ones
+    int high_tile;       // from this one on, key tiles hold keys past some row
+    // Virtual key of logical key j (of the next listed one, if its block is not listed).
+    __device__ __forceinline__ int virt(int j, int bs) const {
+        return j < sinks * bs ? j : max(sinks * bs, j - shift * bs);
+    }
     __device__ __forceinline__ void set(int first, int end, int window, int num_sinks, int bs) {
         lo = max(0, first - window + 1);
         ns = min(num_sinks, lo);
@@ -228,6 +234,9 @@ struct PfWindow {
         const int b = max(lo / bs, sinks);
         shift = b - sinks;
         blocks = sinks + (end - 1) / bs + 1 - b;
+        const int sh = shift * bs, behind = end - 1 - sh - window;  // last virtual key behind the last row's window
+        low_tiles = max((sinks * bs + kBN - 1) / kBN, behind >= 0 ? behind / kBN + 1 : 0);
+        high_tile = (first - sh + 1) / kBN;
     }
 };
 
@@ -705,58 +714,29 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                 tmem_ld_16x256b<8>(tS + 64, s[1]);
                 tmem_wait_ld();
                 if constexpr (WIN) {
-                    // k0 and the limits count virtual keys; kl is the logical key of k0 (past the
-                    // sinks).  A row sees the keys of (pos - window, pos] and the sinks.
-                    const int sk = it.w.sinks * bs, sh = it.w.shift * bs, kl = k0 + sh;
-                    const bool upper = row0_pos - kl < kBN - 1;          // keys past the tile's first row
-                    const bool lower = it.kv_end - 1 - kl >= p.window;   // keys behind the last row's window
-                    if (k0 < sk || (lower && p.num_sinks > kl)) {
-                        const int w0 = pos0 - sh, w1 = pos1 - sh, ns = p.num_sinks - sh;  // virtual, past the sinks
+                    // all in virtual keys: a row sees v <= hi with v >= lo or v < ns (the sinks)
+                    if (j < it.w.low_tiles || j >= it.w.high_tile) {
+                        int r0 = pos0, r1 = pos1;
+                        asm volatile("" : "+r"(r0), "+r"(r1));  // the limits are not kept through the loop
+                        const int hi0 = it.w.virt(r0, bs) - k0, hi1 = it.w.virt(r1, bs) - k0;
+                        const int lo0 = it.w.virt(max(0, r0 - p.window + 1), bs) - k0;
+                        const int lo1 = it.w.virt(max(0, r1 - p.window + 1), bs) - k0;
+                        const int ns = it.w.virt(p.num_sinks, bs) - k0;
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
 #pragma unroll
                             for (int g = 0; g < 8; ++g)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e) {
-                                    const int v = k0 + h * 64 + 8 * g + 2 * ga + e;
-                                    const bool in_sinks = v < sk, first = v < (in_sinks ? p.num_sinks : ns);
-                                    const int q0 = in_sinks ? pos0 : w0, q1 = in_sinks ? pos1 : w1;
-                                    if (v > q0 || (q0 - v >= p.window && !first))
-                                        s[h][4 * g + e] = __float_as_uint(-INFINITY);
-                                    if (v > q1 || (q1 - v >= p.window && !first))
+                                    const int key = h * 64 + 8 * g + 2 * ga + e;
+                                    if (key > hi0 || (key < lo0 && key >= ns)) s[h][4 * g + e] = __float_as_uint(-INFINITY);
+                                    if (key > hi1 || (key < lo1 && key >= ns))
                                         s[h][4 * g + 2 + e] = __float_as_uint(-INFINITY);
                                 }
-                    } else {
-                        if (upper) {
-                            const int lim0 = pos0 - kl, lim1 = pos1 - kl;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int g = 0; g < 8; ++g)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int key = h * 64 + 8 * g + 2 * ga + e;
-                                        if (key > lim0) s[h][4 * g + e] = __float_as_uint(-INFINITY);
-                                        if (key > lim1) s[h][4 * g + 2 + e] = __float_as_uint(-INFINITY);
-                                    }
-                        }
-                        if (lower) {
-                            const int lim0 = pos0 - kl - p.window, lim1 = pos1 - kl - p.window;
-#pragma unroll
-                            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                                for (int g = 0; g < 8; ++g)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int key = h * 64 + 8 * g + 2 * ga + e;
-                                        if (key <= lim0) s[h][4 * g + e] = __float_as_uint(-INFINITY);
-                                        if (key <= lim1) s[h][4 * g + 2 + e] = __float_as_uint(-INFINITY);
-                                    }
-                        }
                     }
-                }
+                } else
                 // mask (keys k0 .. k0+lim-1 are visible to a row; only the last tiles need it)
-                else if (k0 + kBN > row0_pos + 1 || k0 + kBN > it.C) {  // tile-uniform
+                if (k0 + kBN > row0_pos + 1 || k0 + kBN > it.C) {  // tile-uniform
                     const int lim0 = min(pos0 + 1, it.C) - k0, lim1 = min(pos1 + 1, it.C) - k0;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
@@ -850,34 +830,21 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     l0 += rs0.x + rs0.y;
                     l1 += rs1.x + rs1.y;
                 }
-                // keys past kv_end in this tile (not loaded, or past the context): zero V rows,
-                // so that 0-weight rows never meet stale or NaN data
-                auto zero_v = [&](int first, int end) {  // rows [first, end) of the tile
-                    const int st = t % NV;
+                // keys past kv_end in this tile (not loaded, or past the context; WIN: keys
+                // [ns, lo) of the listed blocks too): zero V rows, so that 0-weight rows never meet
+                // stale or NaN data
+                if (WIN ? j < it.w.low_tiles || j >= it.w.high_tile : k0 + kBN > it.kv_end) {
+                    const int valid = it.kv_end - k0 - (WIN ? it.w.shift * bs : 0), st = t % NV;
                     ok = __all_sync(kFullMask, ok && mbar_wait(bar(BVF + st), (t / NV) & 1, p.status));
                     const uint32_t sV = sV0 + st * Sh::KV_BYTES;
                     if (ok)
-                        for (int i = sidx; i < (end - first) * Sh::HALVES * 8; i += 256) {
-                            const int rr = first + i / (Sh::HALVES * 8), rest = i % (Sh::HALVES * 8);
+                        for (int i = WIN ? sidx : sidx + valid * Sh::HALVES * 8; i < kBN * Sh::HALVES * 8; i += 256) {
+                            const int rr = i / (Sh::HALVES * 8), rest = i % (Sh::HALVES * 8);
+                            if (WIN && rr < valid && (k0 + rr < it.w.ns || k0 + rr >= it.w.virt(it.w.lo, bs))) continue;
                             sts128(sV + (rr / 8) * Sh::GSTR + (rest / 8) * 1024 + (rr % 8) * 128 + (rest % 8) * 16, 0u,
                                    0u, 0u, 0u);
                         }
                     fence_async_smem();
-                };
-                if constexpr (WIN) {
-                    // keys of the listed blocks that no row of the tile sees: behind the sinks, in
-                    // front of the window, past the last row (virtual keys, clipped to this tile)
-                    const int sk = it.w.sinks * bs, sh = it.w.shift * bs;
-                    auto clip_zero = [&](int first, int end) {
-                        first = max(first - k0, 0);
-                        end = min(end - k0, kBN);
-                        if (first < end) zero_v(first, end);
-                    };
-                    clip_zero(it.w.ns, min(it.w.lo, sk));
-                    clip_zero(sk, it.w.lo - sh);
-                    clip_zero(it.kv_end - sh, k0 + kBN);
-                } else if (k0 + kBN > it.kv_end) {
-                    zero_v(it.kv_end - k0, kBN);
                 }
                 tc_fence_before();
                 __syncwarp();
