@@ -1,9 +1,677 @@
-// prefill_window.cu -- the instantiations of chunked prefill under a sliding window with
-// sinks; the kernel and its design are in prefill_kernels.cuh.
-#include "prefill_kernels.cuh"
+// prefill_window.cu -- chunked prefill over a sliding window with sinks, on the
+// 5th-generation tensor cores.
+//
+// Row i of a chunk sits at position p = C - Lq + i and sees the keys j <= p with
+// j > p - window or j < num_sinks.  A work item is 128 rows, (token, query head) pairs of one
+// kv head (128/G tokens), of one sequence.
+//
+// What a row can see is bounded by window + num_sinks, so an item walks only the blocks that
+// one of its rows sees: the sinks' blocks, then those from the first row's window to the last
+// row, packed into one list of virtual blocks (a few sinks cost one block, not a key tile)
+// and cut into tiles of 64 virtual keys.  Only tiles at a border are masked.
+//
+// Per key tile: S = Q K^T (tcgen05, fp32 in TMEM, two buffers), the softmax (online, log2
+// domain, the reference moves only when a score exceeds it by 2^8), P in the cache's type
+// over the S columns, O += P V.  The row sums add the rounded weights, as the product does,
+// so that a row that one key dominates loses nothing by the rounding.
+//
+// Under a window items are short (a 1024-key window: nine 128-key tiles), and what costs is
+// what does not overlap: an item's first loads, its last product, its output.  So two CTAs
+// share an SM, each with half of TMEM (two 64-column S buffers and O) and of the shared
+// memory, and one's tiles run under the other's item change; it also gives every scheduler
+// four softmax warps.  Measured (us; 8 chunks of 512 tokens, 64 q / 8 kv heads, window 4096,
+// fp16 | 4 chunks of 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window
+// 301): this 510 | 45 | 28; one CTA per SM with 128-key tiles and three S buffers, as the
+// causal kernel has, 545 | 47 | 42; two CTAs with 128-key tiles and one S buffer each 555 | 57
+// | 40, with S issued for two 64-key tiles at once 574 | 53 | 30; two row tiles per CTA taking
+// turns, one softmax thread per row, 788 | 83 | 67.  What bounds it: with no exponentials, no
+// maxima and no P stores at all (a timing-only build) the first case still took 469 us, the
+// S products of 64 keys reading all of Q from shared memory each time.
+//
+// Warps: 0 TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the rows
+// of V that no row of the item looks at, so that stale or NaN slots never meet a zero
+// weight), 4-11 softmax and output, each a 16-row slab through the 16-lane TMEM shapes.
+// Persistent grid; every mbarrier wait is bounded in time.
+#include <algorithm>
+#include <type_traits>
+
+#include "tcgen05.cuh"
 
 namespace pa {
+namespace {
 
-int launch_prefill_window(const PrefillArgs &a) { return prepare_and_launch<true>(a); }
+constexpr int kThreads = 12 * 32;
+constexpr int kBM = 128, kBN = 64;  // rows of an item, keys of a tile
+constexpr int kSBufs = 2;
+constexpr float kGrowLog2 = 8.f;
+constexpr int kPlanSeqs = 255;       // sequences whose items are listed without gaps
+
+struct Params {
+    void *out;
+    pa_dtype out_dtype;
+    const int32_t *query_start_loc, *block_tables, *context_lens;
+    int max_blocks_per_seq, max_context_len, num_tokens, num_seqs, num_heads, num_kv_heads, block_log2, num_blocks;
+    int window, num_sinks;
+    int group_log2;     // query heads per kv head
+    int units_per_seq;  // items of one kv head in the longest chunk
+    float qk_scale_log2;
+    int32_t *status;
+};
+
+template <int D>
+struct Shape {
+    static constexpr int HALVES = D / 64;            // 128-byte swizzle atoms along D
+    static constexpr int Q_BYTES = kBM * D * 2;      // [half][128 rows][128 B]
+    static constexpr int KV_BYTES = kBN * D * 2;     // one K or V tile: [8-key group][half][8 keys][128 B]
+    static constexpr int GSTR = HALVES * 1024;       // bytes between 8-key groups
+    static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 2;  // K and V stages
+    static constexpr int OFF_K = Q_BYTES;
+    static constexpr int OFF_V = OFF_K + NK * KV_BYTES;
+    static constexpr int OFF_BAR = OFF_V + NV * KV_BYTES;
+    static constexpr int SMEM = 1024 + OFF_BAR + 256 + 4 * (kPlanSeqs + 1);
+    static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// The 16-lane TMEM shapes of 32 columns: four groups of 8 (16x256b), eight of 4 (16x128b).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// mbar_wait (tma.cuh) that lets the hardware suspend the thread for up to a millisecond at a
+// time, for the waits of a role that has run ahead.
+__device__ __forceinline__ bool mbar_wait_idle(uint32_t bar, uint32_t parity, int32_t *status) {
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(1000000u)
+            : "memory");
+        if (done) return true;
+        if (global_ns() - t0 > kWaitLimitNs) {
+            report(status, PA_DEVERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// Query rows and (clamped) context of a sequence; false when it has nothing to compute
+// (reported when `rep`).
+__device__ __forceinline__ bool sequence(const Params &p, int q0, int q1, int C, bool rep, int &ctx) {
+    const int cap = min(p.max_blocks_per_seq << p.block_log2, p.max_context_len);
+    const int Lq = q1 - q0;
+    ctx = C;
+    if (q0 < 0 || q1 < q0 || q1 > p.num_tokens) {  // never index past the query
+        if (rep) report(p.status, PA_DEVERR_QUERY);
+        return false;
+    }
+    if (Lq == 0) return false;
+    if (C > cap) {
+        if (rep) report(p.status, PA_DEVERR_CONTEXT);
+        ctx = cap;
+    }
+    if (Lq > ctx) {
+        if (rep) report(p.status, PA_DEVERR_QUERY);
+        return false;
+    }
+    return true;
+}
+
+// One work item and the keys its rows see.
+struct Item {
+    int s, g, q0, Lq;
+    int tok;            // first chunk token
+    int first, last;    // positions of the first and the last row
+    int ns, lo;         // seen keys: [0, ns) and [lo, last]
+    int sk, sh;         // virtual keys of the sinks' blocks; logical key of virtual v >= sk: v + sh
+    int blocks, tiles;  // virtual blocks, key tiles
+    int low, high;      // tiles < low hold sinks or keys behind some row's window, tiles >= high keys past some row
+
+    // Virtual key of logical key j (of the next listed one, if its block is not listed).
+    __device__ __forceinline__ int virt(int j) const { return j < sk ? j : max(sk, j - sh); }
+};
+
+// The items of a CTA, in order: indexes blockIdx.x, + gridDim.x, ..; index i is unit i / Hkv
+// of kv head i % Hkv, so that the heads that share block-table rows run side by side.
+// fetch() loads the scalars of an item while the one before it is worked on.
+struct Cursor {
+    int64_t idx;
+    int total, s, g, q0, q1, C, unit;
+    const int *plan;  // prefix sums of the sequences' units; null: units_per_seq each
+
+    __device__ __forceinline__ Cursor(const Params &p, const int *plan_) : idx(blockIdx.x), plan(plan_) {
+        total = (plan ? plan[p.num_seqs] : p.num_seqs * p.units_per_seq);
+        fetch(p);
+    }
+    __device__ __forceinline__ bool have(const Params &p) const { return idx < (int64_t)total * p.num_kv_heads; }
+    __device__ __forceinline__ void fetch(const Params &p) {
+        if (!have(p)) return;
+        const int u = (int)(idx / p.num_kv_heads);
+        g = (int)(idx % p.num_kv_heads);
+        if (plan) {
+            int lo = 0, hi = p.num_seqs;  // plan[lo] <= u < plan[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan[mid] <= u) lo = mid; else hi = mid;
+            }
+            s = lo;
+            unit = u - plan[lo];
+        } else {
+            s = u / p.units_per_seq;
+            unit = u % p.units_per_seq;
+        }
+        q0 = p.query_start_loc[s];
+        q1 = p.query_start_loc[s + 1];
+        C = p.context_lens[s];
+    }
+    // The current item (false: no rows), then on to the next.
+    __device__ __forceinline__ bool next(const Params &p, bool rep, Item &it) {
+        int ctx;
+        const bool ok = sequence(p, q0, q1, C, rep, ctx);
+        const int tt = kBM >> p.group_log2, bl = p.block_log2;
+        it.s = s;
+        it.g = g;
+        it.q0 = q0;
+        it.Lq = q1 - q0;
+        it.tok = unit * tt;
+        const bool live = ok && it.tok < it.Lq;
+        if (live) {
+            it.first = ctx - it.Lq + it.tok;
+            it.last = ctx - it.Lq + min(it.Lq, it.tok + tt) - 1;
+            it.lo = max(0, it.first - p.window + 1);
+            it.ns = min(p.num_sinks, it.lo);
+            const int sinks = it.ns > 0 ? ((it.ns - 1) >> bl) + 1 : 0;
+            const int b = max(it.lo >> bl, sinks);
+            it.sk = sinks << bl;
+            it.sh = (b - sinks) << bl;
+            it.blocks = sinks + (it.last >> bl) + 1 - b;
+            const int per_tile = kBN >> bl;
+            it.tiles = (it.blocks + per_tile - 1) / per_tile;
+            const int behind = it.last - it.sh - p.window;  // last virtual key behind the last row's window
+            it.low = max((it.sk + kBN - 1) / kBN, behind >= 0 ? behind / kBN + 1 : 0);
+            it.high = max(0, it.first - it.sh + 1) / kBN;
+        }
+        idx += gridDim.x;
+        fetch(p);
+        return live;
+    }
+};
+
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads, 2)
+prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap, const Params p) {
+    using Sh = Shape<D>;
+    constexpr int NK = Sh::NK, NV = Sh::NV;
+    constexpr bool kBf16 = std::is_same<T, BF16>::value;
+    constexpr uint32_t IDESC_S = mma_idesc(128, kBN, kBf16, false);
+    constexpr uint32_t IDESC_PV = mma_idesc(128, D, kBf16, true);
+    constexpr uint32_t kTmemCols = 256, kTmemO = kSBufs * kBN;  // S (and P) buffers, then O
+    static_assert(kTmemO + D <= kTmemCols, "half of TMEM");
+
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sQ = smem_u32(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Sh::OFF_BAR);
+    const uint32_t b0 = smem_u32(bars);
+    auto bar = [&](int i) { return b0 + 8 * i; };
+    constexpr int BQF = 0;            // Q landed
+    constexpr int BQE = 1;            // last S of that Q finished
+    constexpr int BSF = 2;            // S buffer written
+    constexpr int BPF = BSF + kSBufs; // P written over it
+    constexpr int BPV = BPF + kSBufs; // P.V of that P finished
+    constexpr int BKF = BPV + kSBufs; // K stage landed
+    constexpr int BKE = BKF + NK;     // S of that K finished
+    constexpr int BVF = BKE + NK;     // V stage landed
+    constexpr int BVE = BVF + NV;     // P.V of that V finished
+    constexpr int NBAR = BVE + NV;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
+    int *abort_flag = reinterpret_cast<int *>(bars + NBAR) + 1;
+    int *plan_mem = reinterpret_cast<int *>(smem + Sh::OFF_BAR + 256);
+    static_assert((NBAR + 1) * 8 <= 256, "barrier area");
+
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    if (tid == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i >= BPF && i < BPF + kSBufs ? 8 : 1);
+        fence_barrier_init();
+        prefetch_tensormap(&qmap);
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    pdl_wait_previous();
+    pdl_launch_dependents();
+    const bool planned = p.num_seqs <= kPlanSeqs;
+    if (planned) {  // prefix sums of the sequences' units
+        int units = 0;
+        if (tid < p.num_seqs) {
+            const int q0 = p.query_start_loc[tid], q1 = p.query_start_loc[tid + 1];
+            int ctx;
+            if (sequence(p, q0, q1, p.context_lens[tid], blockIdx.x == 0, ctx))
+                units = min((q1 - q0 - 1) / (kBM >> p.group_log2) + 1, p.units_per_seq);
+        }
+        if (tid < kPlanSeqs + 1) plan_mem[tid] = units;
+        __syncthreads();
+        if (warp == 0) {
+            int carry = 0;
+            for (int base = 0; base <= p.num_seqs; base += 32) {
+                const int i = base + lane, n = i <= kPlanSeqs ? plan_mem[i] : 0;
+                int v = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int w = __shfl_up_sync(kFullMask, v, o);
+                    if (lane >= o) v += w;
+                }
+                if (i <= kPlanSeqs) plan_mem[i] = carry + v - n;
+                carry += __shfl_sync(kFullMask, v, 31);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    volatile int *abort_v = abort_flag;
+    auto wait = [&](int b, uint32_t parity) {
+        return mbar_try_wait(bar(b), parity & 1) || (!*abort_v && mbar_wait_idle(bar(b), parity & 1, p.status));
+    };
+    // Every role walks the same items and counts the same key tiles t over all of them, which
+    // pick ring stages, S buffers and their phases.
+    Cursor cur(p, planned ? plan_mem : nullptr);
+    Item it;
+    int t = 0;
+    bool ok = true;
+
+    if (warp == 0 || warp == 2) {
+        // ============================================ TMA: Q and K, or V
+        const bool is_k = warp == 0;
+        const CUtensorMap *map = is_k ? &kmap : &vmap;
+        const uint32_t ring = sQ + (is_k ? Sh::OFF_K : Sh::OFF_V);
+        const int full = is_k ? BKF : BVF, empty = is_k ? BKE : BVE, NS = is_k ? NK : NV;
+        const uint64_t policy = policy_evict_first();
+        const int bl = p.block_log2, nb = kBN >> bl;  // blocks per key tile (2, 4 or 8)
+        const uint32_t box_bytes = (uint32_t)(D * 2) << bl;
+        int qn = 0;
+        while (ok && cur.have(p)) {
+            if (!cur.next(p, false, it)) continue;
+            const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+            const int sink_blocks = it.sk >> bl, shift = it.sh >> bl;
+            auto block_id = [&](int j) {
+                const int v = j * nb + lane;
+                return lane < nb && v < it.blocks ? bt[v < sink_blocks ? v : v + shift] : -1;
+            };
+            int id0 = block_id(0), id1 = block_id(1);
+            if (is_k) {
+                int q_ok = 1;
+                if (lane == 0) {
+                    q_ok = wait(BQE, qn ^ 1);
+                    if (q_ok) {
+                        mbar_arrive_expect_tx(bar(BQF), Sh::Q_BYTES);
+                        for (int hf = 0; hf < Sh::HALVES; ++hf)
+                            tma_load_3d(sQ + hf * (kBM * 128), &qmap, hf * 64, it.g << p.group_log2, it.q0 + it.tok,
+                                        bar(BQF), policy);
+                    }
+                }
+                ok = __shfl_sync(kFullMask, q_ok, 0);
+                ++qn;
+            }
+            for (int j = 0; ok && j < it.tiles; ++j, ++t) {
+                const int id = id0;
+                id0 = id1;
+                id1 = block_id(j + 2);
+                const bool in_range = lane < nb && j * nb + lane < it.blocks;
+                const bool valid = in_range && id >= 0 && id < p.num_blocks;
+                if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
+                const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
+                const int st = t % NS;
+                int w_ok = 1;
+                if (lane == 0) {
+                    w_ok = wait(empty + st, t / NS + 1);
+                    if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
+                }
+                ok = __shfl_sync(kFullMask, w_ok, 0);
+                if (ok && valid)
+                    tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
+                                bar(full + st), policy);
+                __syncwarp();
+            }
+        }
+        if (!ok) *abort_v = 1;
+    } else if (warp == 1) {
+        // ============================================ S_t = Q K_t^T
+        // S_t overwrites the P of tile t - 2: it waits until that P.V has finished.
+        if (lane == 0) {
+            int qn = 0;
+            while (ok && cur.have(p)) {
+                if (!cur.next(p, false, it)) continue;
+                ok = wait(BQF, qn++);
+                for (int j = 0; ok && j < it.tiles; ++j, ++t) {
+                    const int st = t % NK, sb = t % kSBufs;
+                    ok = wait(BKF + st, t / NK) && wait(BPV + sb, t / kSBufs + 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sK = sQ + Sh::OFF_K + st * Sh::KV_BYTES;
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k)
+                        mma_f16(tmem + sb * kBN, smem_desc(sQ + (k / 4) * (kBM * 128) + (k % 4) * 32, 16, 1024),
+                                smem_desc(sK + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::GSTR), IDESC_S, k > 0);
+                    mma_commit(bar(BSF + sb));
+                    mma_commit(bar(BKE + st));
+                }
+                if (ok) mma_commit(bar(BQE));
+            }
+            if (!ok) *abort_v = 1;
+        }
+    } else if (warp == 3) {
+        // ============================================ O += P_t V_t, P from TMEM
+        while (ok && cur.have(p)) {
+            if (!cur.next(p, false, it)) continue;
+            for (int j = 0; ok && j < it.tiles; ++j, ++t) {
+                const int st = t % NV, pb = t % kSBufs, k0 = j * kBN;
+                const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
+                ok = __all_sync(kFullMask, wait(BVF + st, t / NV));
+                if (ok && (j < it.low || j >= it.high)) {
+                    // rows of V that no row of the item sees: [ns, lo) and past the last row
+                    const int gap0 = it.ns - k0, gap1 = it.virt(it.lo) - k0, end = it.last + 1 - it.sh - k0;
+                    constexpr int VEC = Sh::HALVES * 8;  // 16-byte pieces of a row
+                    if (gap1 > 0 || end < kBN)
+                        for (int i = lane; i < kBN * VEC; i += 32) {
+                            const int r = i / VEC, rest = i % VEC;
+                            if (r < end && (r < gap0 || r >= gap1)) continue;
+                            sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
+                                   0u, 0u);
+                        }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    ok = ok && wait(BPF + pb, t / kSBufs);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < kBN / 16; ++k)
+                            mma_f16_tmem_a(tmem + kTmemO, tmem + pb * kBN + k * 8,
+                                           smem_desc(sV + k * 2 * Sh::GSTR, 1024, Sh::GSTR), IDESC_PV, j > 0 || k > 0);
+                        mma_commit(bar(BPV + pb));
+                        mma_commit(bar(BVE + st));
+                    }
+                }
+                ok = __shfl_sync(kFullMask, (int)ok, 0);
+            }
+        }
+        if (!ok) *abort_v = 1;
+    } else {
+        // ============================================ softmax and output
+        // Warps 4-7 take rows 0-15 and warps 8-11 rows 16-31 of the TMEM lane quarter warp % 4:
+        // a thread holds rows t/4 and t/4 + 8 of its slab, keys 8j + 2(t%4) and the next one of
+        // each group of 8, so a row is spread over four lanes and a thread's pair of keys packs
+        // into the P column 4j + t%4.
+        const int quarter = warp & 3, slab = warp >= 8 ? 1 : 0;
+        const int gi = lane >> 2, ga = lane & 3;
+        const int lane0 = quarter * 32 + slab * 16;    // first TMEM lane (item row) of the slab
+        const int row0 = lane0 + gi, row1 = row0 + 8;  // this thread's rows
+        const uint32_t tL = tmem + ((uint32_t)lane0 << 16), tO = tL + kTmemO;
+        const float sc = p.qk_scale_log2;
+        while (ok && cur.have(p)) {
+            if (!cur.next(p, !planned && warp == 4 && lane == 0, it)) continue;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
+            for (int j = 0; j < it.tiles; ++j, ++t) {
+                const int sb = t % kSBufs;
+                ok = __all_sync(kFullMask, wait(BSF + sb, t / kSBufs));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t tS = tL + sb * kBN;
+                uint32_t s[32];
+                tmem_ld_16x256b<8>(tS, s);
+                tmem_wait_ld();
+                if (j < it.low || j >= it.high) {
+                    // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
+                    // chunk (a ragged last item) as its last row: computed, never stored
+                    const int k0 = j * kBN, ns = it.virt(p.num_sinks) - k0;
+                    const int p0 = min(it.first + (row0 >> p.group_log2), it.last);
+                    const int p1 = min(it.first + (row1 >> p.group_log2), it.last);
+                    const int hi0 = it.virt(p0) - k0, lo0 = it.virt(max(0, p0 - p.window + 1)) - k0;
+                    const int hi1 = it.virt(p1) - k0, lo1 = it.virt(max(0, p1 - p.window + 1)) - k0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = 8 * i + 2 * ga + e;
+                            if (key > hi0 || (key < lo0 && key >= ns)) s[4 * i + e] = __float_as_uint(-INFINITY);
+                            if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
+                        }
+                }
+                // row maxima: 16 scores per row in this lane, then over the row's four lanes
+                float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    a0 = fmax3(a0, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                    c0 = fmax3(c0, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
+                    a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+                    c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
+                }
+                float mx0 = fmaxf(a0, c0), mx1 = fmaxf(a1, c1);
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2)) * sc;
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2)) * sc;
+                const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
+                if (__any_sync(kFullMask, grow0 || grow1)) {  // the four lanes of a row agree
+                    const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
+                    const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
+                    const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
+                    l0 *= f0;
+                    l1 *= f1;
+                    m0 = n0;
+                    m1 = n1;
+                    if (j > 0) {  // O holds the tiles before: wait for the last P.V, scale the rows
+                        ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
+                        if (ok) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[16];
+                                tmem_ld_16x256b_x4(tO + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f0);
+                                    o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f0);
+                                    o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f1);
+                                    o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f1);
+                                }
+                                tmem_st_16x256b_x4(tO + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                }
+                {
+                    const float b0_ = m0 == -INFINITY ? 0.f : m0, b1_ = m1 == -INFINITY ? 0.f : m1;
+                    const float2 sc2 = make_float2(sc, sc), n0 = make_float2(-b0_, -b0_), n1 = make_float2(-b1_, -b1_);
+                    float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                                                     sc2, n0);
+                        const float2 x1 = __ffma2_rn(
+                            make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
+                        w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
+                        w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
+                        r0 = __fadd2_rn(r0, unpack2<T>(w[2 * i]));
+                        r1 = __fadd2_rn(r1, unpack2<T>(w[2 * i + 1]));
+                    }
+                    if (ok) {
+                        tmem_st_16x128b_x8(tS, w);
+                        tmem_wait_st();
+                    }
+                    l0 += r0.x + r0.y;
+                    l1 += r1.x + r1.y;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(BPF + sb));
+            }
+            if (!ok) break;
+            // ---- output.  The next item's first P.V (which overwrites O) waits for P written by
+            // all eight warps after their rows were read here.
+            ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
+            if (!ok) break;
+            tc_fence_after();
+            float L0 = l0 + __shfl_xor_sync(kFullMask, l0, 1), L1 = l1 + __shfl_xor_sync(kFullMask, l1, 1);
+            L0 += __shfl_xor_sync(kFullMask, L0, 2);
+            L1 += __shfl_xor_sync(kFullMask, L1, 2);
+            const float inv0 = L0 > 0.f ? 1.f / L0 : 0.f, inv1 = L1 > 0.f ? 1.f / L1 : 0.f;
+            // one swap with the neighbouring lane gives each lane four consecutive columns, so
+            // that a store instruction writes whole sectors of eight rows
+            const bool odd = (ga & 1) != 0;
+            auto write = [&](auto out_tag) {
+                using OT = decltype(out_tag);
+                OT *outp = static_cast<OT *>(p.out);
+                const int gl = p.group_log2;
+                const int tok0 = it.tok + (row0 >> gl), tok1 = it.tok + (row1 >> gl);
+                const int gm = (1 << gl) - 1, h = it.g << gl;
+                const int64_t base0 = ((int64_t)(it.q0 + tok0) * p.num_heads + h + (row0 & gm)) * D;
+                const int64_t base1 = ((int64_t)(it.q0 + tok1) * p.num_heads + h + (row1 & gm)) * D;
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 64) {
+                    uint32_t r[32];
+                    tmem_ld_16x256b<8>(tO + c0, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int rh = 0; rh < 2; ++rh) {
+                        const float rinv = rh ? inv1 : inv0;
+                        const int64_t base = (rh ? base1 : base0) + c0;
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const int e0 = 4 * i + 2 * rh, e1 = 4 * (i + 1) + 2 * rh;
+                            const float2 near = make_float2(__uint_as_float(r[e0]), __uint_as_float(r[e0 + 1]));
+                            const float2 far = make_float2(__uint_as_float(r[e1]), __uint_as_float(r[e1 + 1]));
+                            const float2 keep = odd ? far : near, send = odd ? near : far;
+                            const float2 got = make_float2(__shfl_xor_sync(kFullMask, send.x, 1),
+                                                           __shfl_xor_sync(kFullMask, send.y, 1));
+                            const int col = odd ? 8 * (i + 1) + 2 * (ga - 1) : 8 * i + 2 * ga;
+                            const float2 a = odd ? got : keep, b = odd ? keep : got;
+                            if ((rh ? tok1 : tok0) >= it.Lq) continue;
+                            if constexpr (std::is_same<OT, float>::value) {
+                                *reinterpret_cast<float4 *>(outp + base + col) =
+                                    make_float4(a.x * rinv, a.y * rinv, b.x * rinv, b.y * rinv);
+                            } else {
+                                using PT = typename std::conditional<std::is_same<OT, __half>::value, F16, BF16>::type;
+                                *reinterpret_cast<uint2 *>(outp + base + col) = make_uint2(
+                                    pack2<PT>(a.x * rinv, a.y * rinv), pack2<PT>(b.x * rinv, b.y * rinv));
+                            }
+                        }
+                    }
+                }
+            };
+            if (p.out_dtype == PA_F32)
+                write(float{});
+            else if (p.out_dtype == PA_F16)
+                write(__half{});
+            else
+                write(__nv_bfloat16{});
+            tc_fence_before();
+        }
+        if (!ok) *abort_v = 1;
+    }
+    // ---- teardown: every TMEM access has completed before the columns are released
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+    }
+}
+
+template <class T, int D>
+int launch_typed(const Params &p, int64_t items, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
+                 cudaStream_t st) {
+    static std::atomic<int> smem_ready[kMaxDevices];  // per device: shared-memory limit raised
+    const int sms = std::max(1, device_sm_count());
+    return launch_pdl_smem(prefill_window_kernel<T, D>, smem_ready, dim3((unsigned)std::min<int64_t>(items, 2 * sms)),
+                           dim3(kThreads), Shape<D>::SMEM, st, qm, km, vm, p) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_prefill_window(const PrefillArgs &a) {
+    Params p{};
+    p.out = a.out;
+    p.out_dtype = a.out_dtype;
+    p.query_start_loc = a.query_start_loc;
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.max_blocks_per_seq = a.max_blocks_per_seq;
+    p.max_context_len = a.max_context_len;
+    p.num_tokens = a.num_tokens;
+    p.num_seqs = a.num_seqs;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.block_log2 = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
+    p.num_blocks = a.num_blocks;
+    p.window = a.window;
+    p.num_sinks = a.num_sinks;
+    const int G = a.num_heads / a.num_kv_heads;
+    p.group_log2 = G == 1 ? 0 : G == 2 ? 1 : G == 4 ? 2 : 3;
+    const int longest = std::min(a.max_query_len, a.num_tokens);
+    p.units_per_seq = (longest - 1) / (kBM / G) + 1;
+    p.qk_scale_log2 = a.scale * kLog2e;
+    p.status = a.status;
+    const int64_t items = (int64_t)a.num_seqs * p.units_per_seq * a.num_kv_heads;
+    const int64_t rows = (int64_t)a.num_blocks * a.block_size;
+    if (rows <= 0 || rows > INT32_MAX || items > INT32_MAX) return PA_ERR_INVALID_ARG;
+    // Q boxes are 64 elements (the swizzle span) wide and cover the G heads of one kv head for
+    // 128/G tokens; a K/V box is one block of one kv head, all of D in 64-wide slices.
+    CUtensorMap qm, km, vm;
+    if (make_tensor_map_3d(&qm, a.query, a.kv_dtype, a.head_dim, a.num_heads, a.num_tokens, 64, G, kBM / G, true) !=
+            PA_OK ||
+        make_kv_block_map(&km, a.key_cache, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, a.block_size) != PA_OK ||
+        make_kv_block_map(&vm, a.value_cache, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, a.block_size) != PA_OK)
+        return PA_ERR_CUDA;
+    switch (a.kv_dtype) {
+        case PA_F16:
+            return a.head_dim == 64 ? launch_typed<F16, 64>(p, items, qm, km, vm, a.stream)
+                                    : launch_typed<F16, 128>(p, items, qm, km, vm, a.stream);
+        case PA_BF16:
+            return a.head_dim == 64 ? launch_typed<BF16, 64>(p, items, qm, km, vm, a.stream)
+                                    : launch_typed<BF16, 128>(p, items, qm, km, vm, a.stream);
+        default: return PA_ERR_UNSUPPORTED;
+    }
+}
 
 }  // namespace pa
