@@ -276,73 +276,92 @@ def _refuse(what: str, why: str) -> None:
     raise PAError(-1, f"{what}: {why}")
 
 
-def _call(dev: torch.device, stream, name, *args) -> None:
-    """Call a C entry point, stream last, with the tensors' device current (a stream given must
-    be of it).  Without one: torch's current stream of that device."""
-    f = getattr(_lib, name)
-    i = dev.index
-    if i == torch._C._cuda_getDevice():
-        code = f(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            code = f(*args, torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream))
-    if code != 0:
-        raise PAError(code, name)
+# The calls below run with their tensors' device current (a stream given must be of it) and,
+# without a stream, on torch's current stream of that device.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)  # absent from builds without CUDA
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _check_window(what, out, query, key_cache, value_cache, tables, lens, starts, status) -> torch.device:
-    """Shapes, types, layout and device of the windowed calls' tensors; returns the device."""
-    if query.dim() != 3 or key_cache.dim() != 4 or tables.dim() != 2 or lens.dim() != 1:
+def _check_window(what, out, query, key_cache, value_cache, tables, lens, starts, status):
+    """Shapes, types, layout and device of the windowed calls' tensors; returns the shapes of
+    query, key_cache and block_tables, the cache's dtype code and the device's index."""
+    qs, ks, ts, ls = query.shape, key_cache.shape, tables.shape, lens.shape
+    if len(qs) != 3 or len(ks) != 4 or len(ts) != 2 or len(ls) != 1:
         _refuse(what, "query is [T][Hq][D], a cache [NB][bs][Hkv][D], block_tables [S][max_blocks], lengths [S]")
-    if out.shape != query.shape or key_cache.shape != value_cache.shape or query.shape[2] != key_cache.shape[3]:
+    if out.shape != qs or value_cache.shape != ks or qs[2] != ks[3]:
         _refuse(what, "out is shaped as query, value_cache as key_cache, head dims are equal")
-    dt = query.dtype
-    if key_cache.dtype != dt or value_cache.dtype != dt:
+    dt, i32 = query.dtype, torch.int32
+    if key_cache.dtype is not dt or value_cache.dtype is not dt:
         _refuse(what, "query and caches share one dtype")
-    i32 = torch.int32
-    if tables.dtype != i32 or lens.dtype != i32 or (starts is not None and starts.dtype != i32) or (
-            status is not None and status.dtype != i32):
+    if tables.dtype is not i32 or lens.dtype is not i32:
         _refuse(what, "tables, lengths, starts and status are int32")
-    rows = lens.shape[0]
-    if tables.shape[0] != rows or (query.shape[0] != rows if starts is None else starts.shape != (rows + 1,)):
+    rows = ls[0]
+    if ts[0] != rows or (starts is None and qs[0] != rows):
         _refuse(what, "one table row and length per sequence, one query row each or S + 1 row starts")
     if not (out.is_contiguous() and query.is_contiguous() and key_cache.is_contiguous() and
-            value_cache.is_contiguous() and tables.is_contiguous() and lens.is_contiguous() and
-            (starts is None or starts.is_contiguous())):
+            value_cache.is_contiguous() and tables.is_contiguous() and lens.is_contiguous()):
         _refuse(what, "tensors must be contiguous")
-    dev = query.device
-    if dev.type != "cuda" or not (out.device == dev == key_cache.device == value_cache.device == tables.device ==
-                                  lens.device) or (starts is not None and starts.device != dev) or (
-            status is not None and status.device != dev):
+    dev = query.get_device()
+    if dev < 0 or not (out.get_device() == dev == key_cache.get_device() == value_cache.get_device() ==
+                       tables.get_device() == lens.get_device()):
         _refuse(what, "tensors must be on one CUDA device")
-    return dev
+    if starts is not None:
+        if starts.dtype is not i32:
+            _refuse(what, "tables, lengths, starts and status are int32")
+        if starts.shape != (rows + 1,):
+            _refuse(what, "one table row and length per sequence, one query row each or S + 1 row starts")
+        if not starts.is_contiguous():
+            _refuse(what, "tensors must be contiguous")
+        if starts.get_device() != dev:
+            _refuse(what, "tensors must be on one CUDA device")
+    if status is not None:
+        if status.dtype is not i32 or status.numel() < 1:
+            _refuse(what, "tables, lengths, starts and status are int32")
+        if status.get_device() != dev:
+            _refuse(what, "tensors must be on one CUDA device")
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return qs, ks, ts[1], code, dev
 
 
 def pa_decode_window(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len: int,
                      window: int, num_sinks: int, scale: float, *, status=None, stream=None) -> None:
     """pa_decode over the newest ``window`` keys and the first ``num_sinks`` of each sequence.
     No workspace; table entries of blocks that no key is seen in are not read."""
-    dev = _check_window("pa_decode_window", out, query, key_cache, value_cache, block_tables, context_lens, None, status)
-    S, Hq, D = query.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    _call(dev, stream, "pa_decode_window", out.data_ptr(), _dt(out), query.data_ptr(), key_cache.data_ptr(),
-          value_cache.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-          int(max_context_len), int(window), int(num_sinks), S, Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache),
-          _ptr(status))
+    (S, Hq, D), (NB, bs, Hkv, _), width, code, dev = _check_window(
+        "pa_decode_window", out, query, key_cache, value_cache, block_tables, context_lens, None, status)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_decode_window(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
+                                    window, num_sinks, scale, status=status, stream=stream)
+    rc = _lib.pa_decode_window(
+        out.data_ptr(), _dt(out), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        block_tables.data_ptr(), width, context_lens.data_ptr(), int(max_context_len), int(window), int(num_sinks), S,
+        Hq, Hkv, D, bs, NB, scale, code, None if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream))
+    if rc != 0:
+        raise PAError(rc, "pa_decode_window")
 
 
 def pa_prefill_window(out, query, query_start_loc, max_query_len: int, key_cache, value_cache, block_tables,
                       context_lens, max_context_len: int, window: int, num_sinks: int, scale: float, *, status=None,
                       stream=None) -> None:
     """pa_prefill_chunk over the newest ``window`` keys before each row and the first ``num_sinks``."""
-    dev = _check_window("pa_prefill_window", out, query, key_cache, value_cache, block_tables, context_lens,
-                        query_start_loc, status)
-    Tq, Hq, D = query.shape
-    NB, bs, Hkv, _ = key_cache.shape
-    _call(dev, stream, "pa_prefill_window", out.data_ptr(), _dt(out), query.data_ptr(), query_start_loc.data_ptr(), Tq,
-          int(max_query_len), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
-          block_tables.shape[1], context_lens.data_ptr(), int(max_context_len), int(window), int(num_sinks),
-          context_lens.shape[0], Hq, Hkv, D, bs, NB, float(scale), _dt(key_cache), _ptr(status))
+    (Tq, Hq, D), (NB, bs, Hkv, _), width, code, dev = _check_window(
+        "pa_prefill_window", out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, status)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_prefill_window(out, query, query_start_loc, max_query_len, key_cache, value_cache, block_tables,
+                                     context_lens, max_context_len, window, num_sinks, scale, status=status,
+                                     stream=stream)
+    rc = _lib.pa_prefill_window(
+        out.data_ptr(), _dt(out), query.data_ptr(), query_start_loc.data_ptr(), Tq, int(max_query_len),
+        key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
+        int(max_context_len), int(window), int(num_sinks), context_lens.shape[0], Hq, Hkv, D, bs, NB, scale, code,
+        None if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream))
+    if rc != 0:
+        raise PAError(rc, "pa_prefill_window")
 
 
 # ----------------------------------------------------------------------------- rotary axes
@@ -386,28 +405,30 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
     what = "pa_reshape_and_cache_rope_axes"
     if (query is None) != (query_out is None):
         _refuse(what, "query and query_out go together")
-    if key.dim() != 3 or key_cache.dim() != 4 or key.shape != value.shape or key_cache.shape != value_cache.shape or (
-            key.shape[1:] != key_cache.shape[2:]):
+    shape, ks = key.shape, key_cache.shape
+    if len(shape) != 3 or len(ks) != 4 or value.shape != shape or value_cache.shape != ks or shape[1:] != ks[2:]:
         _refuse(what, "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
-    T, Hkv, D = key.shape
-    NB, bs = key_cache.shape[:2]
-    dt, dev = key.dtype, key.device
+    (T, Hkv, D), dt, dev = shape, key.dtype, key.get_device()
+    one_device = (dev >= 0 and value.get_device() == dev == key_cache.get_device() == value_cache.get_device() ==
+                  slot_mapping.get_device() == positions.get_device() == rope.freqs.get_device())
     Hq = q_stride = 0
     if query is not None:
-        if query.dim() != 3 or query.shape != query_out.shape or query.shape[0] != T or query.shape[2] != D:
+        qs = query.shape
+        if len(qs) != 3 or query_out.shape != qs or qs[0] != T or qs[2] != D:
             _refuse(what, "query and query_out are [T][Hq][D]")
-        Hq = query.shape[1]
+        Hq = qs[1]
         q_stride, q_head, q_one = query.stride()
-        if query.dtype != dt or query_out.dtype != dt:
+        if query.dtype is not dt or query_out.dtype is not dt:
             _refuse(what, "query, keys, values and caches share one dtype")
         if T and (q_one != 1 or (Hq > 1 and q_head != D)):
             _refuse(what, "a token's heads must be contiguous")
         if not query_out.is_contiguous():
             _refuse(what, "caches, query_out, slots and positions must be contiguous")
-    if value.dtype != dt or key_cache.dtype != dt or value_cache.dtype != dt:
+        one_device = one_device and query.get_device() == dev == query_out.get_device()
+    if value.dtype is not dt or key_cache.dtype is not dt or value_cache.dtype is not dt:
         _refuse(what, "query, keys, values and caches share one dtype")
-    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,) or positions.dtype != torch.int32 or (
-            positions.shape != (rope.num_axes, T)) or (status is not None and status.dtype != torch.int32):
+    if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,) or positions.dtype is not torch.int32 or (
+            positions.shape != (rope.num_axes, T)) or (status is not None and status.dtype is not torch.int32):
         _refuse(what, "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32")
     if not (key_cache.is_contiguous() and value_cache.is_contiguous() and slot_mapping.is_contiguous() and
             positions.is_contiguous()):
@@ -416,11 +437,19 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
     v_stride, v_head, v_one = value.stride()
     if T and (k_one != 1 or v_one != 1 or (Hkv > 1 and (k_head != D or v_head != D))):
         _refuse(what, "a token's heads must be contiguous")
-    if dev.type != "cuda" or not (value.device == dev == key_cache.device == value_cache.device ==
-                                  slot_mapping.device == positions.device == rope.freqs.device) or (
-            query is not None and not (query.device == dev == query_out.device)) or (
-            status is not None and status.device != dev):
+    if not one_device or (status is not None and status.get_device() != dev):
         _refuse(what, "tensors must be on one CUDA device")
-    _call(dev, stream, what, _ptr(query_out), _ptr(query), key.data_ptr(), value.data_ptr(), key_cache.data_ptr(),
-          value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(), T, Hq, Hkv, D, q_stride, k_stride,
-          v_stride, bs, NB, _dt(key_cache), ctypes.byref(rope._c()), _ptr(status))
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, value_cache, slot_mapping,
+                                                  positions, rope, status=status, stream=stream)
+    rc = _lib.pa_reshape_and_cache_rope_axes(
+        None if query is None else query_out.data_ptr(), None if query is None else query.data_ptr(), key.data_ptr(),
+        value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
+        T, Hq, Hkv, D, q_stride, k_stride, v_stride, ks[1], ks[0], code, ctypes.byref(rope._c()),
+        None if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream))
+    if rc != 0:
+        raise PAError(rc, what)
