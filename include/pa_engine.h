@@ -61,6 +61,16 @@ int pa_engine_attend(const pa_engine_cache *cache, const pa_sched_batch *batch,
                      const void *k, const void *v, void *out, pa_dtype out_dtype, void *workspace,
                      size_t workspace_bytes, int32_t *status, pa_stream_t stream);
 
+/*
+ * pa_engine_attend_window -- pa_engine_attend under a sliding window with sinks: the same
+ * block copies and cache write (pa_reshape_and_cache), then pa_decode_window or
+ * pa_prefill_window with `window` and `num_sinks` (their rules; no workspace).
+ */
+int pa_engine_attend_window(const pa_engine_cache *cache, int window, int num_sinks,
+                            const pa_sched_batch *batch, const pa_sched_offsets *offsets,
+                            const void *dev_batch, const void *q, const void *k, const void *v,
+                            void *out, pa_dtype out_dtype, int32_t *status, pa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

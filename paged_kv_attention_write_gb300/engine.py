@@ -6,8 +6,8 @@ the C++ scheduler writes the whole batch description into one pinned host buffer
 (``pa_sched_step_packed``), its device part goes over in one asynchronous copy
 (``pa_engine_upload``), and one more call (``pa_engine_attend``) enqueues the step's
 copy-on-write block copies, the fresh K/V written into the paged cache and decode or
-chunked-prefill attention, reading the batch from that copy.  The model
-side is supplied by the caller: ``qkv(step)`` returns the device tensors q ``[T][Hq][D]``, k and
+chunked-prefill attention, reading the batch from that copy (``pa_engine_attend_window`` when
+the engine is made with a sliding window).  The model side is supplied by the caller: ``qkv(step)`` returns the device tensors q ``[T][Hq][D]``, k and
 v ``[T][Hkv][D]`` of the step's query tokens (``step`` holds their token ids and positions, on
 the host and, through ``device_tokens``, on the device), ``sample(step, out)`` returns one next
 token per sequence.  Marshalling only: every computation on the data runs in the library's
@@ -39,6 +39,11 @@ _lib.pa_engine_attend.argtypes = [ctypes.POINTER(_Cache), ctypes.POINTER(_Batch)
                                   ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
                                   ctypes.c_void_p, ctypes.c_void_p]
 _lib.pa_engine_attend.restype = ctypes.c_int
+_lib.pa_engine_attend_window.argtypes = [ctypes.POINTER(_Cache), ctypes.c_int, ctypes.c_int, ctypes.POINTER(_Batch),
+                                         ctypes.POINTER(_Offsets), ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.c_void_p, ctypes.c_void_p]
+_lib.pa_engine_attend_window.restype = ctypes.c_int
 
 __all__ = ["PagedAttentionEngine"]
 
@@ -49,7 +54,12 @@ class PagedAttentionEngine:
     def __init__(self, num_blocks: int, block_size: int, num_heads: int, num_kv_heads: int,
                  head_dim: int, dtype: torch.dtype = torch.bfloat16, device="cuda",
                  token_budget: int = 4096, chunk_tokens: int = 512, max_decode_steps: int = 8,
-                 prefix_cache: bool = True, scale: Optional[float] = None):
+                 prefix_cache: bool = True, scale: Optional[float] = None, window: Optional[int] = None,
+                 num_sinks: int = 0):
+        """``window``: attend the newest ``window`` keys and the first ``num_sinks`` only."""
+        if (window is not None and window < 1) or num_sinks < 0 or (num_sinks and window is None):
+            raise ValueError("window is at least 1, num_sinks at least 0 and only with a window")
+        self.window, self.num_sinks = window, num_sinks
         self.sched = Scheduler(num_blocks, block_size, token_budget, chunk_tokens, max_decode_steps,
                                prefix_cache)
         self.dev = torch.device(device)
@@ -133,14 +143,20 @@ class PagedAttentionEngine:
                                     dtype=torch.float32, device=self.dev)
         out = self._out[:T]
         ws, ws_bytes = None, 0
-        if b.kind == 2:  # decode: a workspace for the split of the contexts
+        if b.kind == 2 and self.window is None:  # decode: a workspace for the split of the contexts
             need = max(1, pa_decode_workspace_size(S, self.Hq, self.Hkv, self.D, b.max_context_len))
             if self._ws is None or self._ws.numel() < need:
                 self._ws = torch.empty(need * 2, dtype=torch.uint8, device=self.dev)
             ws, ws_bytes = self._ws.data_ptr(), self._ws.numel()
-        _check(_lib.pa_engine_attend(ctypes.byref(self._cache), ctypes.byref(b), ctypes.byref(o),
-                                     self._dev_buf.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     out.data_ptr(), _PA_F32, ws, ws_bytes, None, stream), "pa_engine_attend")
+        if self.window is None:
+            _check(_lib.pa_engine_attend(ctypes.byref(self._cache), ctypes.byref(b), ctypes.byref(o),
+                                         self._dev_buf.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                         out.data_ptr(), _PA_F32, ws, ws_bytes, None, stream), "pa_engine_attend")
+        else:
+            _check(_lib.pa_engine_attend_window(ctypes.byref(self._cache), self.window, self.num_sinks,
+                                                ctypes.byref(b), ctypes.byref(o), self._dev_buf.data_ptr(),
+                                                q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _PA_F32,
+                                                None, stream), "pa_engine_attend_window")
         step["out"] = out
         self.sched.complete(sample(step, out))
         return step
