@@ -54,6 +54,7 @@ struct Params {
     int window, num_sinks;
     int group_log2;     // query heads per kv head
     int units_per_seq;  // items of one kv head in the longest chunk
+    int listed;         // ragged chunks: items are numbered without gaps (else every sequence has units_per_seq)
     float qk_scale_log2;
     int32_t *status;
 };
@@ -154,71 +155,35 @@ struct Item {
     __device__ __forceinline__ int virt(int j) const { return j < sk ? j : max(sk, j - sh); }
 };
 
-// The items of a CTA, in order: indexes blockIdx.x, + gridDim.x, ..; index i is unit i / Hkv
-// of kv head i % Hkv, so that the heads that share block-table rows run side by side.
-// fetch() loads the scalars of an item while the one before it is worked on.
-struct Cursor {
-    int64_t idx;
-    int total, s, g, q0, q1, C, unit;
-    const int *plan;  // prefix sums of the sequences' units; null: units_per_seq each
-
-    __device__ __forceinline__ Cursor(const Params &p, const int *plan_) : idx(blockIdx.x), plan(plan_) {
-        total = (plan ? plan[p.num_seqs] : p.num_seqs * p.units_per_seq);
-        fetch(p);
-    }
-    __device__ __forceinline__ bool have(const Params &p) const { return idx < (int64_t)total * p.num_kv_heads; }
-    __device__ __forceinline__ void fetch(const Params &p) {
-        if (!have(p)) return;
-        const int u = (int)(idx / p.num_kv_heads);
-        g = (int)(idx % p.num_kv_heads);
-        if (plan) {
-            int lo = 0, hi = p.num_seqs;  // plan[lo] <= u < plan[hi]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (plan[mid] <= u) lo = mid; else hi = mid;
-            }
-            s = lo;
-            unit = u - plan[lo];
-        } else {
-            s = u / p.units_per_seq;
-            unit = u % p.units_per_seq;
-        }
-        q0 = p.query_start_loc[s];
-        q1 = p.query_start_loc[s + 1];
-        C = p.context_lens[s];
-    }
-    // The current item (false: no rows), then on to the next.
-    __device__ __forceinline__ bool next(const Params &p, bool rep, Item &it) {
-        int ctx;
-        const bool ok = sequence(p, q0, q1, C, rep, ctx);
-        const int tt = kBM >> p.group_log2, bl = p.block_log2;
-        it.s = s;
-        it.g = g;
-        it.q0 = q0;
-        it.Lq = q1 - q0;
-        it.tok = unit * tt;
-        const bool live = ok && it.tok < it.Lq;
-        if (live) {
-            it.first = ctx - it.Lq + it.tok;
-            it.last = ctx - it.Lq + min(it.Lq, it.tok + tt) - 1;
-            it.lo = max(0, it.first - p.window + 1);
-            it.ns = min(p.num_sinks, it.lo);
-            const int sinks = it.ns > 0 ? ((it.ns - 1) >> bl) + 1 : 0;
-            const int b = max(it.lo >> bl, sinks);
-            it.sk = sinks << bl;
-            it.sh = (b - sinks) << bl;
-            it.blocks = sinks + (it.last >> bl) + 1 - b;
-            const int per_tile = kBN >> bl;
-            it.tiles = (it.blocks + per_tile - 1) / per_tile;
-            const int behind = it.last - it.sh - p.window;  // last virtual key behind the last row's window
-            it.low = max((it.sk + kBN - 1) / kBN, behind >= 0 ? behind / kBN + 1 : 0);
-            it.high = max(0, it.first - it.sh + 1) / kBN;
-        }
-        idx += gridDim.x;
-        fetch(p);
-        return live;
-    }
-};
+// The work item of this CTA: unit and kv head of sequence s (unit: 128 rows of the chunk);
+// false when it has no rows.
+__device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int g, bool rep, Item &it) {
+    const int q0 = p.query_start_loc[s], q1 = p.query_start_loc[s + 1];
+    int ctx;
+    const bool ok = sequence(p, q0, q1, p.context_lens[s], rep, ctx);
+    const int tt = kBM >> p.group_log2, bl = p.block_log2;
+    it.s = s;
+    it.g = g;
+    it.q0 = q0;
+    it.Lq = q1 - q0;
+    it.tok = unit * tt;
+    if (!ok || it.tok >= it.Lq) return false;
+    it.first = ctx - it.Lq + it.tok;
+    it.last = ctx - it.Lq + min(it.Lq, it.tok + tt) - 1;
+    it.lo = max(0, it.first - p.window + 1);
+    it.ns = min(p.num_sinks, it.lo);
+    const int sinks = it.ns > 0 ? ((it.ns - 1) >> bl) + 1 : 0;
+    const int b = max(it.lo >> bl, sinks);
+    it.sk = sinks << bl;
+    it.sh = (b - sinks) << bl;
+    it.blocks = sinks + (it.last >> bl) + 1 - b;
+    const int per_tile = kBN >> bl;
+    it.tiles = (it.blocks + per_tile - 1) / per_tile;
+    const int behind = it.last - it.sh - p.window;  // last virtual key behind the last row's window
+    it.low = max((it.sk + kBN - 1) / kBN, behind >= 0 ? behind / kBN + 1 : 0);
+    it.high = max(0, it.first - it.sh + 1) / kBN;
+    return true;
+}
 
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -240,8 +205,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const uint32_t b0 = smem_u32(bars);
     auto bar = [&](int i) { return b0 + 8 * i; };
     constexpr int BQF = 0;            // Q landed
-    constexpr int BQE = 1;            // last S of that Q finished
-    constexpr int BSF = 2;            // S buffer written
+    constexpr int BSF = 1;            // S buffer written
     constexpr int BPF = BSF + kSBufs; // P written over it
     constexpr int BPV = BPF + kSBufs; // P.V of that P finished
     constexpr int BKF = BPV + kSBufs; // K stage landed
@@ -270,8 +234,12 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     pdl_wait_previous();
     pdl_launch_dependents();
-    const bool planned = p.num_seqs <= kPlanSeqs;
-    if (planned) {  // prefix sums of the sequences' units
+    // CTAs are numbered sequence by sequence (the items of one share their keys in L2), from a
+    // chunk's last rows to its first (the first rows of a fresh prompt see few keys), kv heads
+    // side by side.
+    const int idx = (int)(blockIdx.x / (unsigned)p.num_kv_heads), g = (int)(blockIdx.x % (unsigned)p.num_kv_heads);
+    int seq, unit;
+    if (p.listed) {  // prefix sums of the sequences' units
         int units = 0;
         if (tid < p.num_seqs) {
             const int q0 = p.query_start_loc[tid], q1 = p.query_start_loc[tid + 1];
@@ -295,7 +263,21 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                 carry += __shfl_sync(kFullMask, v, 31);
             }
         }
+        __syncthreads();
+        const int u = plan_mem[p.num_seqs] - 1 - idx;
+        int lo = 0, hi = p.num_seqs;  // plan_mem[lo] <= u < plan_mem[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (plan_mem[mid] <= u) lo = mid; else hi = mid;
+        }
+        seq = lo;
+        unit = u < 0 ? INT32_MAX >> 8 : u - plan_mem[lo];  // past the last item: no such rows
+    } else {
+        seq = idx / p.units_per_seq;
+        unit = p.units_per_seq - 1 - idx % p.units_per_seq;
     }
+    Item it;
+    const bool live = make_item(p, seq, unit, g, !p.listed && unit == 0 && g == 0 && tid == 0, it);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -304,14 +286,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     auto wait = [&](int b, uint32_t parity) {
         return mbar_try_wait(bar(b), parity & 1) || (!*abort_v && mbar_wait_idle(bar(b), parity & 1, p.status));
     };
-    // Every role walks the same items and counts the same key tiles t over all of them, which
-    // pick ring stages, S buffers and their phases.
-    Cursor cur(p, planned ? plan_mem : nullptr);
-    Item it;
-    int t = 0;
     bool ok = true;
 
-    if (warp == 0 || warp == 2) {
+    if (!live) {
+        // no rows: every warp goes straight to the teardown
+    } else if (warp == 0 || warp == 2) {
         // ============================================ TMA: Q and K, or V
         const bool is_k = warp == 0;
         const CUtensorMap *map = is_k ? &kmap : &vmap;
@@ -320,113 +299,93 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         const uint64_t policy = policy_evict_first();
         const int bl = p.block_log2, nb = kBN >> bl;  // blocks per key tile (2, 4 or 8)
         const uint32_t box_bytes = (uint32_t)(D * 2) << bl;
-        int qn = 0;
-        while (ok && cur.have(p)) {
-            if (!cur.next(p, false, it)) continue;
-            const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
-            const int sink_blocks = it.sk >> bl, shift = it.sh >> bl;
-            auto block_id = [&](int j) {
-                const int v = j * nb + lane;
-                return lane < nb && v < it.blocks ? bt[v < sink_blocks ? v : v + shift] : -1;
-            };
-            int id0 = block_id(0), id1 = block_id(1);
-            if (is_k) {
-                int q_ok = 1;
-                if (lane == 0) {
-                    q_ok = wait(BQE, qn ^ 1);
-                    if (q_ok) {
-                        mbar_arrive_expect_tx(bar(BQF), Sh::Q_BYTES);
-                        for (int hf = 0; hf < Sh::HALVES; ++hf)
-                            tma_load_3d(sQ + hf * (kBM * 128), &qmap, hf * 64, it.g << p.group_log2, it.q0 + it.tok,
-                                        bar(BQF), policy);
-                    }
-                }
-                ok = __shfl_sync(kFullMask, q_ok, 0);
-                ++qn;
+        const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+        const int sink_blocks = it.sk >> bl, shift = it.sh >> bl;
+        auto block_id = [&](int j) {
+            const int v = j * nb + lane;
+            return lane < nb && v < it.blocks ? bt[v < sink_blocks ? v : v + shift] : -1;
+        };
+        int id0 = block_id(0), id1 = block_id(1);
+        if (is_k && lane == 0) {
+            mbar_arrive_expect_tx(bar(BQF), Sh::Q_BYTES);
+            for (int hf = 0; hf < Sh::HALVES; ++hf)
+                tma_load_3d(sQ + hf * (kBM * 128), &qmap, hf * 64, it.g << p.group_log2, it.q0 + it.tok, bar(BQF),
+                            policy);
+        }
+        for (int t = 0; ok && t < it.tiles; ++t) {
+            const int id = id0;
+            id0 = id1;
+            id1 = block_id(t + 2);
+            const bool in_range = lane < nb && t * nb + lane < it.blocks;
+            const bool valid = in_range && id >= 0 && id < p.num_blocks;
+            if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
+            const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
+            const int st = t % NS;
+            int w_ok = 1;
+            if (lane == 0) {
+                w_ok = wait(empty + st, t / NS + 1);
+                if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
             }
-            for (int j = 0; ok && j < it.tiles; ++j, ++t) {
-                const int id = id0;
-                id0 = id1;
-                id1 = block_id(j + 2);
-                const bool in_range = lane < nb && j * nb + lane < it.blocks;
-                const bool valid = in_range && id >= 0 && id < p.num_blocks;
-                if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
-                const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
-                const int st = t % NS;
-                int w_ok = 1;
-                if (lane == 0) {
-                    w_ok = wait(empty + st, t / NS + 1);
-                    if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
-                }
-                ok = __shfl_sync(kFullMask, w_ok, 0);
-                if (ok && valid)
-                    tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
-                                bar(full + st), policy);
-                __syncwarp();
-            }
+            ok = __shfl_sync(kFullMask, w_ok, 0);
+            if (ok && valid)
+                tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
+                            bar(full + st), policy);
+            __syncwarp();
         }
         if (!ok) *abort_v = 1;
     } else if (warp == 1) {
         // ============================================ S_t = Q K_t^T
         // S_t overwrites the P of tile t - 2: it waits until that P.V has finished.
         if (lane == 0) {
-            int qn = 0;
-            while (ok && cur.have(p)) {
-                if (!cur.next(p, false, it)) continue;
-                ok = wait(BQF, qn++);
-                for (int j = 0; ok && j < it.tiles; ++j, ++t) {
-                    const int st = t % NK, sb = t % kSBufs;
-                    ok = wait(BKF + st, t / NK) && wait(BPV + sb, t / kSBufs + 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sK = sQ + Sh::OFF_K + st * Sh::KV_BYTES;
+            ok = wait(BQF, 0);
+            for (int t = 0; ok && t < it.tiles; ++t) {
+                const int st = t % NK, sb = t % kSBufs;
+                ok = wait(BKF + st, t / NK) && wait(BPV + sb, t / kSBufs + 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sK = sQ + Sh::OFF_K + st * Sh::KV_BYTES;
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        mma_f16(tmem + sb * kBN, smem_desc(sQ + (k / 4) * (kBM * 128) + (k % 4) * 32, 16, 1024),
-                                smem_desc(sK + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::GSTR), IDESC_S, k > 0);
-                    mma_commit(bar(BSF + sb));
-                    mma_commit(bar(BKE + st));
-                }
-                if (ok) mma_commit(bar(BQE));
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16(tmem + sb * kBN, smem_desc(sQ + (k / 4) * (kBM * 128) + (k % 4) * 32, 16, 1024),
+                            smem_desc(sK + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::GSTR), IDESC_S, k > 0);
+                mma_commit(bar(BSF + sb));
+                mma_commit(bar(BKE + st));
             }
             if (!ok) *abort_v = 1;
         }
     } else if (warp == 3) {
         // ============================================ O += P_t V_t, P from TMEM
-        while (ok && cur.have(p)) {
-            if (!cur.next(p, false, it)) continue;
-            for (int j = 0; ok && j < it.tiles; ++j, ++t) {
-                const int st = t % NV, pb = t % kSBufs, k0 = j * kBN;
-                const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
-                ok = __all_sync(kFullMask, wait(BVF + st, t / NV));
-                if (ok && (j < it.low || j >= it.high)) {
-                    // rows of V that no row of the item sees: [ns, lo) and past the last row
-                    const int gap0 = it.ns - k0, gap1 = it.virt(it.lo) - k0, end = it.last + 1 - it.sh - k0;
-                    constexpr int VEC = Sh::HALVES * 8;  // 16-byte pieces of a row
-                    if (gap1 > 0 || end < kBN)
-                        for (int i = lane; i < kBN * VEC; i += 32) {
-                            const int r = i / VEC, rest = i % VEC;
-                            if (r < end && (r < gap0 || r >= gap1)) continue;
-                            sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
-                                   0u, 0u);
-                        }
-                    fence_async_smem();
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    ok = ok && wait(BPF + pb, t / kSBufs);
-                    if (ok) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int k = 0; k < kBN / 16; ++k)
-                            mma_f16_tmem_a(tmem + kTmemO, tmem + pb * kBN + k * 8,
-                                           smem_desc(sV + k * 2 * Sh::GSTR, 1024, Sh::GSTR), IDESC_PV, j > 0 || k > 0);
-                        mma_commit(bar(BPV + pb));
-                        mma_commit(bar(BVE + st));
+        for (int t = 0; ok && t < it.tiles; ++t) {
+            const int st = t % NV, pb = t % kSBufs, k0 = t * kBN;
+            const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
+            ok = __all_sync(kFullMask, wait(BVF + st, t / NV));
+            if (ok && (t < it.low || t >= it.high)) {
+                // rows of V that no row of the item sees: [ns, lo) and past the last row
+                const int gap0 = it.ns - k0, gap1 = it.virt(it.lo) - k0, end = it.last + 1 - it.sh - k0;
+                constexpr int VEC = Sh::HALVES * 8;  // 16-byte pieces of a row
+                if (gap1 > 0 || end < kBN)
+                    for (int i = lane; i < kBN * VEC; i += 32) {
+                        const int r = i / VEC, rest = i % VEC;
+                        if (r < end && (r < gap0 || r >= gap1)) continue;
+                        sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
+                               0u, 0u);
                     }
-                }
-                ok = __shfl_sync(kFullMask, (int)ok, 0);
+                fence_async_smem();
+                __syncwarp();
             }
+            if (lane == 0) {
+                ok = ok && wait(BPF + pb, t / kSBufs);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < kBN / 16; ++k)
+                        mma_f16_tmem_a(tmem + kTmemO, tmem + pb * kBN + k * 8,
+                                       smem_desc(sV + k * 2 * Sh::GSTR, 1024, Sh::GSTR), IDESC_PV, t > 0 || k > 0);
+                    mma_commit(bar(BPV + pb));
+                    mma_commit(bar(BVE + st));
+                }
+            }
+            ok = __shfl_sync(kFullMask, (int)ok, 0);
         }
         if (!ok) *abort_v = 1;
     } else {
@@ -441,113 +400,110 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         const int row0 = lane0 + gi, row1 = row0 + 8;  // this thread's rows
         const uint32_t tL = tmem + ((uint32_t)lane0 << 16), tO = tL + kTmemO;
         const float sc = p.qk_scale_log2;
-        while (ok && cur.have(p)) {
-            if (!cur.next(p, !planned && warp == 4 && lane == 0, it)) continue;
-            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
-            for (int j = 0; j < it.tiles; ++j, ++t) {
-                const int sb = t % kSBufs;
-                ok = __all_sync(kFullMask, wait(BSF + sb, t / kSBufs));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t tS = tL + sb * kBN;
-                uint32_t s[32];
-                tmem_ld_16x256b<8>(tS, s);
-                tmem_wait_ld();
-                if (j < it.low || j >= it.high) {
-                    // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
-                    // chunk (a ragged last item) as its last row: computed, never stored
-                    const int k0 = j * kBN, ns = it.virt(p.num_sinks) - k0;
-                    const int p0 = min(it.first + (row0 >> p.group_log2), it.last);
-                    const int p1 = min(it.first + (row1 >> p.group_log2), it.last);
-                    const int hi0 = it.virt(p0) - k0, lo0 = it.virt(max(0, p0 - p.window + 1)) - k0;
-                    const int hi1 = it.virt(p1) - k0, lo1 = it.virt(max(0, p1 - p.window + 1)) - k0;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
+        int t = 0;
+        for (; t < it.tiles; ++t) {
+            const int sb = t % kSBufs;
+            ok = __all_sync(kFullMask, wait(BSF + sb, t / kSBufs));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t tS = tL + sb * kBN;
+            uint32_t s[32];
+            tmem_ld_16x256b<8>(tS, s);
+            tmem_wait_ld();
+            if (t < it.low || t >= it.high) {
+                // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
+                // chunk (a ragged last item) as its last row: computed, never stored
+                const int k0 = t * kBN, ns = it.virt(p.num_sinks) - k0;
+                const int p0 = min(it.first + (row0 >> p.group_log2), it.last);
+                const int p1 = min(it.first + (row1 >> p.group_log2), it.last);
+                const int hi0 = it.virt(p0) - k0, lo0 = it.virt(max(0, p0 - p.window + 1)) - k0;
+                const int hi1 = it.virt(p1) - k0, lo1 = it.virt(max(0, p1 - p.window + 1)) - k0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 8; ++i)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int key = 8 * i + 2 * ga + e;
-                            if (key > hi0 || (key < lo0 && key >= ns)) s[4 * i + e] = __float_as_uint(-INFINITY);
-                            if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
-                        }
-                }
-                // row maxima: 16 scores per row in this lane, then over the row's four lanes
-                float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < 8; i += 2) {
-                    a0 = fmax3(a0, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
-                    c0 = fmax3(c0, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
-                    a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
-                    c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
-                }
-                float mx0 = fmaxf(a0, c0), mx1 = fmaxf(a1, c1);
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2)) * sc;
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2)) * sc;
-                const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
-                if (__any_sync(kFullMask, grow0 || grow1)) {  // the four lanes of a row agree
-                    const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
-                    const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
-                    const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
-                    l0 *= f0;
-                    l1 *= f1;
-                    m0 = n0;
-                    m1 = n1;
-                    if (j > 0) {  // O holds the tiles before: wait for the last P.V, scale the rows
-                        ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
-                        if (ok) {
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 32) {
-                                uint32_t o[16];
-                                tmem_ld_16x256b_x4(tO + c, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f0);
-                                    o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f0);
-                                    o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f1);
-                                    o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f1);
-                                }
-                                tmem_st_16x256b_x4(tO + c, o);
-                            }
-                            tmem_wait_st();
-                        }
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = 8 * i + 2 * ga + e;
+                        if (key > hi0 || (key < lo0 && key >= ns)) s[4 * i + e] = __float_as_uint(-INFINITY);
+                        if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
                     }
-                }
-                {
-                    const float b0_ = m0 == -INFINITY ? 0.f : m0, b1_ = m1 == -INFINITY ? 0.f : m1;
-                    const float2 sc2 = make_float2(sc, sc), n0 = make_float2(-b0_, -b0_), n1 = make_float2(-b1_, -b1_);
-                    float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
-                    uint32_t w[16];
+            }
+            // row maxima: 16 scores per row in this lane, then over the row's four lanes
+            float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
-                                                     sc2, n0);
-                        const float2 x1 = __ffma2_rn(
-                            make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
-                        w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
-                        w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
-                        r0 = __fadd2_rn(r0, unpack2<T>(w[2 * i]));
-                        r1 = __fadd2_rn(r1, unpack2<T>(w[2 * i + 1]));
-                    }
+            for (int i = 0; i < 8; i += 2) {
+                a0 = fmax3(a0, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                c0 = fmax3(c0, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
+                a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+                c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
+            }
+            float mx0 = fmaxf(a0, c0), mx1 = fmaxf(a1, c1);
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2)) * sc;
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2)) * sc;
+            const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
+            if (__any_sync(kFullMask, grow0 || grow1)) {  // the four lanes of a row agree
+                const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
+                const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
+                const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
+                l0 *= f0;
+                l1 *= f1;
+                m0 = n0;
+                m1 = n1;
+                if (t > 0) {  // O holds the tiles before: wait for the last P.V, scale the rows
+                    ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
                     if (ok) {
-                        tmem_st_16x128b_x8(tS, w);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[16];
+                            tmem_ld_16x256b_x4(tO + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f0);
+                                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f0);
+                                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f1);
+                                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f1);
+                            }
+                            tmem_st_16x256b_x4(tO + c, o);
+                        }
                         tmem_wait_st();
                     }
-                    l0 += r0.x + r0.y;
-                    l1 += r1.x + r1.y;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (!ok) break;
-                if (lane == 0) mbar_arrive(bar(BPF + sb));
             }
+            {
+                const float b0_ = m0 == -INFINITY ? 0.f : m0, b1_ = m1 == -INFINITY ? 0.f : m1;
+                const float2 sc2 = make_float2(sc, sc), n0 = make_float2(-b0_, -b0_), n1 = make_float2(-b1_, -b1_);
+                float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                                                 sc2, n0);
+                    const float2 x1 = __ffma2_rn(
+                        make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
+                    w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
+                    w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
+                    r0 = __fadd2_rn(r0, unpack2<T>(w[2 * i]));
+                    r1 = __fadd2_rn(r1, unpack2<T>(w[2 * i + 1]));
+                }
+                if (ok) {
+                    tmem_st_16x128b_x8(tS, w);
+                    tmem_wait_st();
+                }
+                l0 += r0.x + r0.y;
+                l1 += r1.x + r1.y;
+            }
+            tc_fence_before();
+            __syncwarp();
             if (!ok) break;
-            // ---- output.  The next item's first P.V (which overwrites O) waits for P written by
-            // all eight warps after their rows were read here.
-            ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
-            if (!ok) break;
+            if (lane == 0) mbar_arrive(bar(BPF + sb));
+        }
+        // ---- output
+        ok = ok && __all_sync(kFullMask, wait(BPV + (it.tiles - 1) % kSBufs, (it.tiles - 1) / kSBufs));
+        if (ok) {
             tc_fence_after();
             float L0 = l0 + __shfl_xor_sync(kFullMask, l0, 1), L1 = l1 + __shfl_xor_sync(kFullMask, l1, 1);
             L0 += __shfl_xor_sync(kFullMask, L0, 2);
@@ -620,8 +576,7 @@ template <class T, int D>
 int launch_typed(const Params &p, int64_t items, const CUtensorMap &qm, const CUtensorMap &km, const CUtensorMap &vm,
                  cudaStream_t st) {
     static std::atomic<int> smem_ready[kMaxDevices];  // per device: shared-memory limit raised
-    const int sms = std::max(1, device_sm_count());
-    return launch_pdl_smem(prefill_window_kernel<T, D>, smem_ready, dim3((unsigned)std::min<int64_t>(items, 2 * sms)),
+    return launch_pdl_smem(prefill_window_kernel<T, D>, smem_ready, dim3((unsigned)items),
                            dim3(kThreads), Shape<D>::SMEM, st, qm, km, vm, p) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
@@ -652,7 +607,12 @@ int launch_prefill_window(const PrefillArgs &a) {
     p.units_per_seq = (longest - 1) / (kBM / G) + 1;
     p.qk_scale_log2 = a.scale * kLog2e;
     p.status = a.status;
-    const int64_t items = (int64_t)a.num_seqs * p.units_per_seq * a.num_kv_heads;
+    // Chunks of one length fill num_seqs * units_per_seq items.  Ragged ones are numbered without
+    // gaps, as long as the sequences fit the list: at most one item of each is not whole.
+    const int64_t uniform = (int64_t)a.num_seqs * p.units_per_seq;
+    const int64_t most = a.num_tokens / (kBM / G) + (int64_t)a.num_seqs;
+    p.listed = a.num_seqs <= kPlanSeqs && most < uniform;
+    const int64_t items = (p.listed ? most : uniform) * a.num_kv_heads;
     const int64_t rows = (int64_t)a.num_blocks * a.block_size;
     if (rows <= 0 || rows > INT32_MAX || items > INT32_MAX) return PA_ERR_INVALID_ARG;
     // Q boxes are 64 elements (the swizzle span) wide and cover the G heads of one kv head for
