@@ -363,7 +363,7 @@ int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const voi
  * position context_lens[s] - Lq_s + i.  Arguments, invalid chunks and dtypes (F16, BF16) as
  * for pa_prefill_chunk.  Values at the positions that some row of a chunk sees must be
  * finite (a key that one row sees and another does not enters the second row's sum with
- * weight zero).
+ * weight zero).  How a row's keys are split depends on the call's sizes alone.
  */
 int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
                       const int32_t *query_start_loc, int num_tokens, int max_query_len,

@@ -214,6 +214,25 @@ def test_prefill_many_ragged_chunks(dtype, D):
     check(prefill, make_case(dtype, 8, 2, D, 8, ctx, 333, 7, chunks=chunks, seed=7), dtype, True)
 
 
+@pytest.mark.parametrize("D,bs,Hkv,G", [(128, 16, 1, 8), (64, 32, 2, 1), (128, 8, 2, 4)])
+@pytest.mark.parametrize("window,sinks", [(4096, 16), (700, 0), (1 << 30, 5)])
+def test_prefill_few_rows_behind_long_windows(D, bs, Hkv, G, window, sinks):
+    # few items: their keys are split over the CTAs of a cluster
+    case = make_case(BF16, Hkv * G, Hkv, D, bs, [6000, 130, 300], window, sinks, chunks=[45, 1, 3], seed=D + window % 97)
+    check(prefill, case, FP32, True)
+    check(prefill, case, BF16, True)
+
+
+def test_prefill_split_items_report_a_bad_block():
+    case = make_case(BF16, 8, 2, 128, 16, [3000, 500], 2048, 4, chunks=[20, 9], seed=31)
+    t = case.cuda()
+    good = prefill(case, t=t)
+    t["tables"][0, 150] = -1
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = prefill(case, t=t, status=status)
+    assert status.item() == 2 and torch.equal(out[20:], good[20:])
+
+
 def test_prefill_reports_bad_chunks_and_blocks():
     case = make_case(BF16, 8, 2, 64, 8, [200, 300, 150], 60, 4, chunks=[40, 50, 60], seed=8)
     t = case.cuda()
