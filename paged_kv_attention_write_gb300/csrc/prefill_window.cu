@@ -317,7 +317,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         const CUtensorMap *map = is_k ? &kmap : &vmap;
         const uint32_t ring = sQ + (is_k ? Sh::OFF_K : Sh::OFF_V);
         const int full = is_k ? BKF : BVF, empty = is_k ? BKE : BVE, NS = is_k ? NK : NV;
-        const uint64_t policy = policy_evict_first();
+        // keys and values are read again by the next items of the sequence
+        const uint64_t policy = policy_evict_normal();
         const int bl = p.block_log2, nb = kBN >> bl;  // blocks per key tile (2, 4 or 8)
         const uint32_t box_bytes = (uint32_t)(D * 2) << bl;
         const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
@@ -448,7 +449,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                         if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
                     }
             }
-            // row maxima: 16 scores per row in this lane, then over the row's four lanes
+            // maximum of the 16 scores per row in this lane
             float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
@@ -457,13 +458,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                 a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
                 c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
             }
-            float mx0 = fmaxf(a0, c0), mx1 = fmaxf(a1, c1);
-            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
-            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2)) * sc;
-            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2)) * sc;
-            const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
-            if (__any_sync(kFullMask, grow0 || grow1)) {  // the four lanes of a row agree
+            float mx0 = fmaxf(a0, c0) * sc, mx1 = fmaxf(a1, c1) * sc;
+            if (__any_sync(kFullMask, mx0 > m0 + kGrowLog2 || mx1 > m1 + kGrowLog2)) {
+                // the row's maximum, the same in its four lanes
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
+                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2));
+                const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
                 const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
                 const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
                 const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
