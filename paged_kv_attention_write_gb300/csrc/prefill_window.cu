@@ -225,7 +225,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     constexpr int BKE = BKF + NK;     // S of that K finished
     constexpr int BVF = BKE + NK;     // V stage landed
     constexpr int BVE = BVF + NV;     // P.V of that V finished
-    constexpr int NBAR = BVE + NV;
+    constexpr int BTM = BVE + NV;     // TMEM allocated
+    constexpr int NBAR = BTM + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     int *abort_flag = reinterpret_cast<int *>(bars + NBAR) + 1;
     int *plan_mem = reinterpret_cast<int *>(smem + Sh::OFF_BAR + 256);
@@ -240,11 +241,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         prefetch_tensormap(&kmap);
         prefetch_tensormap(&vmap);
     }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                     "r"(kTmemCols));
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
+    __syncthreads();  // barriers initialised
     pdl_wait_previous();
     pdl_launch_dependents();
     // CTAs are numbered sequence by sequence (the items of one share their keys in L2), from a
@@ -292,13 +289,17 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     Item it{};
     const bool live = make_item(p, seq, unit, g, !p.listed && unit == 0 && g == 0 && tid == 0, it);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     volatile int *abort_v = abort_flag;
     auto wait = [&](int b, uint32_t parity) {
         return mbar_try_wait(bar(b), parity & 1) || (!*abort_v && mbar_wait_idle(bar(b), parity & 1, p.status));
+    };
+    // The loads do not wait for TMEM: warp 1 allocates it while they are under way.
+    uint32_t tmem = 0;
+    auto wait_tmem = [&]() {
+        const bool got = __all_sync(kFullMask, wait(BTM, 0));
+        tc_fence_after();
+        tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+        return got;
     };
     // this CTA's key tiles: j0 + t, t < n
     int j0 = 0, n = it.tiles;
@@ -358,7 +359,15 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     } else if (warp == 1) {
         // ============================================ S_t = Q K_t^T
         // S_t overwrites the P of tile t - 2: it waits until that P.V has finished.
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+        tc_fence_before();
+        __syncwarp();
         if (lane == 0) {
+            mbar_arrive(bar(BTM));
             ok = wait(BQF, 0);
             for (int t = 0; ok && t < n; ++t) {
                 const int st = t % NK, sb = t % kSBufs;
@@ -377,6 +386,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
     } else if (warp == 3) {
         // ============================================ O += P_t V_t, P from TMEM
+        ok = wait_tmem();
         for (int t = 0; ok && t < n; ++t) {
             const int st = t % NV, pb = t % kSBufs, k0 = (j0 + t) * kBN;
             const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
@@ -420,10 +430,11 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         const int gi = lane >> 2, ga = lane & 3;
         const int lane0 = quarter * 32 + slab * 16;    // first TMEM lane (item row) of the slab
         const int row0 = lane0 + gi, row1 = row0 + 8;  // this thread's rows
+        ok = wait_tmem();
         const uint32_t tL = tmem + ((uint32_t)lane0 << 16), tO = tL + kTmemO;
         const float sc = p.qk_scale_log2;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
-        for (int t = 0; t < n; ++t) {
+        for (int t = 0; ok && t < n; ++t) {
             const int sb = t % kSBufs;
             ok = __all_sync(kFullMask, wait(BSF + sb, t / kSBufs));
             if (!ok) break;
@@ -581,21 +592,23 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             const int e0 = 4 * i + 2 * rh, e1 = 4 * (i + 1) + 2 * rh;
-                            const float2 near = make_float2(__uint_as_float(r[e0]), __uint_as_float(r[e0 + 1]));
-                            const float2 far = make_float2(__uint_as_float(r[e1]), __uint_as_float(r[e1 + 1]));
-                            const float2 keep = odd ? far : near, send = odd ? near : far;
-                            const float2 got = make_float2(__shfl_xor_sync(kFullMask, send.x, 1),
-                                                           __shfl_xor_sync(kFullMask, send.y, 1));
+                            const float2 near = make_float2(__uint_as_float(r[e0]) * rinv, __uint_as_float(r[e0 + 1]) * rinv);
+                            const float2 far = make_float2(__uint_as_float(r[e1]) * rinv, __uint_as_float(r[e1 + 1]) * rinv);
                             const int col = odd ? 8 * (i + 1) + 2 * (ga - 1) : 8 * i + 2 * ga;
-                            const float2 a = odd ? got : keep, b = odd ? keep : got;
-                            if ((rh ? tok1 : tok0) >= it.Lq) continue;
+                            const bool inside = (rh ? tok1 : tok0) < it.Lq;
                             if constexpr (std::is_same<OT, float>::value) {
-                                *reinterpret_cast<float4 *>(outp + base + col) =
-                                    make_float4(a.x * rinv, a.y * rinv, b.x * rinv, b.y * rinv);
+                                const float2 keep = odd ? far : near, send = odd ? near : far;
+                                const float2 got = make_float2(__shfl_xor_sync(kFullMask, send.x, 1),
+                                                               __shfl_xor_sync(kFullMask, send.y, 1));
+                                const float2 a = odd ? got : keep, b = odd ? keep : got;
+                                if (inside) *reinterpret_cast<float4 *>(outp + base + col) = make_float4(a.x, a.y, b.x, b.y);
                             } else {
                                 using PT = typename std::conditional<std::is_same<OT, __half>::value, F16, BF16>::type;
-                                *reinterpret_cast<uint2 *>(outp + base + col) = make_uint2(
-                                    pack2<PT>(a.x * rinv, a.y * rinv), pack2<PT>(b.x * rinv, b.y * rinv));
+                                const uint32_t wn = pack2<PT>(near.x, near.y), wf = pack2<PT>(far.x, far.y);
+                                const uint32_t got = __shfl_xor_sync(kFullMask, odd ? wn : wf, 1);
+                                if (inside)
+                                    *reinterpret_cast<uint2 *>(outp + base + col) =
+                                        odd ? make_uint2(got, wf) : make_uint2(wn, got);
                             }
                         }
                     }
@@ -655,7 +668,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (live && warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
