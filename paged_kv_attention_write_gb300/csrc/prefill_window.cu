@@ -50,7 +50,6 @@ namespace {
 
 constexpr int kThreads = 12 * 32;
 constexpr int kBM = 128, kBN = 64;  // rows of an item, keys of a tile
-constexpr int kSBufs = 2;
 constexpr float kGrowLog2 = 8.f;
 constexpr int kPlanSeqs = 255;       // sequences whose items are listed without gaps
 
@@ -67,6 +66,21 @@ struct Params {
     int32_t *status;
 };
 
+// r += the two weights packed in w, each widened exactly inside the add (mixed-precision add).
+template <class T>
+__device__ __forceinline__ void add_pair(float2 &r, uint32_t w) {
+    if constexpr (std::is_same<T, BF16>::value)
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "add.rn.f32.bf16 %0, l, %0;\n\tadd.rn.f32.bf16 %1, h, %1;\n\t}"
+            : "+f"(r.x), "+f"(r.y)
+            : "r"(w));
+    else
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "add.rn.f32.f16 %0, l, %0;\n\tadd.rn.f32.f16 %1, h, %1;\n\t}"
+            : "+f"(r.x), "+f"(r.y)
+            : "r"(w));
+}
+
 template <int D>
 struct Shape {
     static constexpr int HALVES = D / 64;            // 128-byte swizzle atoms along D
@@ -74,6 +88,7 @@ struct Shape {
     static constexpr int KV_BYTES = kBN * D * 2;     // one K or V tile: [8-key group][half][8 keys][128 B]
     static constexpr int GSTR = HALVES * 1024;       // bytes between 8-key groups
     static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 2;  // K and V stages
+    static constexpr int SBUFS = D == 64 ? 3 : 2;   // S buffers in TMEM, beside O
     static constexpr int OFF_K = Q_BYTES;
     static constexpr int OFF_V = OFF_K + NK * KV_BYTES;
     static constexpr int OFF_BAR = OFF_V + NV * KV_BYTES;
@@ -203,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const Params p) {
     using Sh = Shape<D>;
-    constexpr int NK = Sh::NK, NV = Sh::NV;
+    constexpr int NK = Sh::NK, NV = Sh::NV, kSBufs = Sh::SBUFS;
     constexpr bool kBf16 = std::is_same<T, BF16>::value;
     constexpr uint32_t IDESC_S = mma_idesc(128, kBN, kBf16, false);
     constexpr uint32_t IDESC_PV = mma_idesc(128, D, kBf16, true);
@@ -519,8 +534,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                         make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
                     w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
                     w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
-                    r0 = __fadd2_rn(r0, unpack2<T>(w[2 * i]));
-                    r1 = __fadd2_rn(r1, unpack2<T>(w[2 * i + 1]));
+                    add_pair<T>(r0, w[2 * i]);
+                    add_pair<T>(r1, w[2 * i + 1]);
                 }
                 if (ok) {
                     tmem_st_16x128b_x8(tS, w);
