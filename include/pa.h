@@ -425,6 +425,43 @@ int pa_reshape_and_cache_rope_axes(void *query_out, const void *query, const voi
                                    int block_size, int num_blocks, pa_dtype kv_dtype,
                                    const pa_rope_axes *rope, int32_t *status, pa_stream_t stream);
 
+/*
+ * The same three calls with their arguments in one record, for bindings whose foreign calls
+ * pay for every argument.  A field means what the argument of its name does;
+ * pa_decode_window_args reads neither query_start_loc, num_tokens nor max_query_len, and
+ * pa_reshape_and_cache_rope_axes_args takes the fields of pa_rope_axes beside the others.  A
+ * NULL record returns PA_ERR_INVALID_ARG.
+ */
+typedef struct {
+    void *out;
+    const void *query, *key_cache, *value_cache;
+    const int32_t *query_start_loc, *block_tables, *context_lens;
+    int32_t *status;
+    pa_stream_t stream;
+    int32_t out_dtype, kv_dtype, num_tokens, max_query_len, max_blocks_per_seq, max_context_len;
+    int32_t window, num_sinks, num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+    float scale;
+} pa_window_args;
+
+typedef struct {
+    void *query_out;
+    const void *query, *key, *value;
+    void *key_cache, *value_cache;
+    const int64_t *slot_mapping;
+    const int32_t *positions;
+    const float *freqs;
+    const int32_t *pair_axis;
+    int32_t *status;
+    pa_stream_t stream;
+    int64_t query_stride, key_stride, value_stride;
+    int32_t num_tokens, num_heads, num_kv_heads, head_dim, block_size, num_blocks, kv_dtype;
+    int32_t rope_dim, num_axes, halves;
+} pa_rope_axes_args;
+
+int pa_decode_window_args(const pa_window_args *args);
+int pa_prefill_window_args(const pa_window_args *args);
+int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *args);
+
 /* Static description of a PA_* return code. */
 const char *pa_status_string(int code);
 

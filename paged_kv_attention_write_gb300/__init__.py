@@ -24,6 +24,7 @@ Operations (see ``include/pa.h`` for layouts, ownership and error behaviour):
 from __future__ import annotations
 
 import ctypes
+import struct
 from pathlib import Path
 from typing import Optional
 
@@ -77,23 +78,27 @@ _lib.pa_decode_rope.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, 
                                 _i32, _i32, _f32, _i32, ctypes.POINTER(_PaRope), _vp, _sz, _vp, _vp]
 
 
-class _PaRopeAxes(ctypes.Structure):
-    _fields_ = [("freqs", _vp), ("pair_axis", _vp), ("rope_dim", _i32), ("num_axes", _i32), ("halves", _i32)]
+def _send(name: str, f, record: struct.Struct, *fields) -> None:
+    try:
+        args = record.pack(*fields)
+    except struct.error as e:  # not an integer, or one past 32 bits
+        raise PAError(-1, f"{name}: {e}") from None
+    rc = f(args)
+    if rc != 0:
+        raise PAError(rc, name)
 
 
-_i64 = ctypes.c_int64
-_lib.pa_decode_window.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
-                                  _i32, _i32, _i32, _f32, _i32, _vp, _vp]
-_lib.pa_prefill_window.argtypes = [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
-                                   _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp, _vp]
+# The windowed and multi-axis calls go over as one packed record each (pa_window_args,
+# pa_rope_axes_args): ctypes takes about as long for their twenty arguments as the launch does.
+_WINDOW_ARGS = struct.Struct("@9P14if4x")
+_ROPE_AXES_ARGS = struct.Struct("@12P3q10i")
+for _name in ("pa_decode_window_args", "pa_prefill_window_args", "pa_reshape_and_cache_rope_axes_args"):
+    getattr(_lib, _name).argtypes = [ctypes.c_char_p]
+    getattr(_lib, _name).restype = _i32
 _lib.pa_rope_pair_axes.argtypes = [_vp, _i32, _vp, _i32, _i32]
-_lib.pa_reshape_and_cache_rope_axes.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32,
-                                                _i64, _i64, _i64, _i32, _i32, _i32, ctypes.POINTER(_PaRopeAxes),
-                                                _vp, _vp]
 for _name in ("pa_reshape_and_cache", "pa_decode", "pa_decode_noalloc", "pa_prefill_chunk",
               "pa_copy_blocks", "pa_version", "pa_rope_yarn_freqs", "pa_reshape_and_cache_rope",
-              "pa_decode_rope", "pa_decode_write", "pa_decode_window", "pa_prefill_window",
-              "pa_rope_pair_axes", "pa_reshape_and_cache_rope_axes"):
+              "pa_decode_rope", "pa_decode_write", "pa_rope_pair_axes"):
     getattr(_lib, _name).restype = _i32
 
 
@@ -335,13 +340,11 @@ def pa_decode_window(out, query, key_cache, value_cache, block_tables, context_l
         with torch.cuda.device(dev):
             return pa_decode_window(out, query, key_cache, value_cache, block_tables, context_lens, max_context_len,
                                     window, num_sinks, scale, status=status, stream=stream)
-    rc = _lib.pa_decode_window(
-        out.data_ptr(), _dt(out), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-        block_tables.data_ptr(), width, context_lens.data_ptr(), int(max_context_len), int(window), int(num_sinks), S,
-        Hq, Hkv, D, bs, NB, scale, code, None if status is None else status.data_ptr(),
-        _current_stream(dev) if stream is None else _stream(stream))
-    if rc != 0:
-        raise PAError(rc, "pa_decode_window")
+    _send("pa_decode_window", _lib.pa_decode_window_args, _WINDOW_ARGS,
+        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), 0, block_tables.data_ptr(),
+        context_lens.data_ptr(), 0 if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream), _dt(out), code, S, 1, width, max_context_len,
+        window, num_sinks, S, Hq, Hkv, D, bs, NB, scale)
 
 
 def pa_prefill_window(out, query, query_start_loc, max_query_len: int, key_cache, value_cache, block_tables,
@@ -355,13 +358,11 @@ def pa_prefill_window(out, query, query_start_loc, max_query_len: int, key_cache
             return pa_prefill_window(out, query, query_start_loc, max_query_len, key_cache, value_cache, block_tables,
                                      context_lens, max_context_len, window, num_sinks, scale, status=status,
                                      stream=stream)
-    rc = _lib.pa_prefill_window(
-        out.data_ptr(), _dt(out), query.data_ptr(), query_start_loc.data_ptr(), Tq, int(max_query_len),
-        key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(), width, context_lens.data_ptr(),
-        int(max_context_len), int(window), int(num_sinks), context_lens.shape[0], Hq, Hkv, D, bs, NB, scale, code,
-        None if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream))
-    if rc != 0:
-        raise PAError(rc, "pa_prefill_window")
+    _send("pa_prefill_window", _lib.pa_prefill_window_args, _WINDOW_ARGS,
+        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), query_start_loc.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), 0 if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream), _dt(out), code, Tq, max_query_len, width,
+        max_context_len, window, num_sinks, context_lens.shape[0], Hq, Hkv, D, bs, NB, scale)
 
 
 # ----------------------------------------------------------------------------- rotary axes
@@ -384,16 +385,13 @@ class RopeAxes:
 
     def __init__(self, freqs: torch.Tensor, pair_axis: torch.Tensor, rope_dim: int, num_axes: int,
                  halves: bool = False):
-        n = rope_dim // 2
-        if not (freqs.dtype == torch.float32 and pair_axis.dtype == torch.int32 and rope_dim % 2 == 0 and
-                freqs.shape == (n,) and pair_axis.shape == (n,) and freqs.is_contiguous() and
-                pair_axis.is_contiguous() and freqs.device == pair_axis.device):
+        shape = (rope_dim // 2,)
+        if not (freqs.dtype is torch.float32 and pair_axis.dtype is torch.int32 and rope_dim % 2 == 0 and
+                freqs.shape == shape and pair_axis.shape == shape and freqs.is_contiguous() and
+                pair_axis.is_contiguous() and freqs.get_device() == pair_axis.get_device()):
             _refuse("RopeAxes", "freqs is fp32 and pair_axis int32, both [rope_dim / 2], dense, on one device")
         self.freqs, self.pair_axis = freqs, pair_axis
         self.rope_dim, self.num_axes, self.halves = int(rope_dim), int(num_axes), bool(halves)
-
-    def _c(self):
-        return _PaRopeAxes(self.freqs.data_ptr(), self.pair_axis.data_ptr(), self.rope_dim, self.num_axes, self.halves)
 
 
 def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, value_cache, slot_mapping, positions,
@@ -446,10 +444,9 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
         with torch.cuda.device(dev):
             return pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, value_cache, slot_mapping,
                                                   positions, rope, status=status, stream=stream)
-    rc = _lib.pa_reshape_and_cache_rope_axes(
-        None if query is None else query_out.data_ptr(), None if query is None else query.data_ptr(), key.data_ptr(),
+    _send(what, _lib.pa_reshape_and_cache_rope_axes_args, _ROPE_AXES_ARGS,
+        0 if query is None else query_out.data_ptr(), 0 if query is None else query.data_ptr(), key.data_ptr(),
         value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
-        T, Hq, Hkv, D, q_stride, k_stride, v_stride, ks[1], ks[0], code, ctypes.byref(rope._c()),
-        None if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream))
-    if rc != 0:
-        raise PAError(rc, what)
+        rope.freqs.data_ptr(), rope.pair_axis.data_ptr(), 0 if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream), q_stride, k_stride, v_stride, T, Hq, Hkv, D,
+        ks[1], ks[0], code, rope.rope_dim, rope.num_axes, rope.halves)

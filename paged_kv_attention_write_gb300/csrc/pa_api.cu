@@ -358,4 +358,30 @@ int pa_reshape_and_cache_rope_axes(void *query_out, const void *query, const voi
     return pa::launch_reshape_and_cache_rope_axes(a);
 }
 
+int pa_decode_window_args(const pa_window_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return pa_decode_window(a->out, (pa_dtype)a->out_dtype, a->query, a->key_cache, a->value_cache, a->block_tables,
+                            a->max_blocks_per_seq, a->context_lens, a->max_context_len, a->window, a->num_sinks,
+                            a->num_seqs, a->num_heads, a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks,
+                            a->scale, (pa_dtype)a->kv_dtype, a->status, a->stream);
+}
+
+int pa_prefill_window_args(const pa_window_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return pa_prefill_window(a->out, (pa_dtype)a->out_dtype, a->query, a->query_start_loc, a->num_tokens,
+                             a->max_query_len, a->key_cache, a->value_cache, a->block_tables, a->max_blocks_per_seq,
+                             a->context_lens, a->max_context_len, a->window, a->num_sinks, a->num_seqs, a->num_heads,
+                             a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks, a->scale,
+                             (pa_dtype)a->kv_dtype, a->status, a->stream);
+}
+
+int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const pa_rope_axes rope{a->freqs, a->pair_axis, a->rope_dim, a->num_axes, a->halves};
+    return pa_reshape_and_cache_rope_axes(a->query_out, a->query, a->key, a->value, a->key_cache, a->value_cache,
+                                          a->slot_mapping, a->positions, a->num_tokens, a->num_heads, a->num_kv_heads,
+                                          a->head_dim, a->query_stride, a->key_stride, a->value_stride, a->block_size,
+                                          a->num_blocks, (pa_dtype)a->kv_dtype, &rope, a->status, a->stream);
+}
+
 }  // extern "C"

@@ -195,6 +195,38 @@ def test_windowed_python_refusals(pa, over, why):
         pa.pa_prefill_window(**a)
 
 
+def test_record_calls_refuse_what_the_flat_ones_do(lib, pa):
+    assert lib.pa_decode_window_args(None) == lib.pa_prefill_window_args(None) == -1
+    assert lib.pa_reshape_and_cache_rope_axes_args(None) == -1
+
+    def window(f, out_dtype=2, kv_dtype=2, T=64, mq=64, window=10, sinks=2, S=2, Hq=32, D=128, query=FAKE, scale=0.1):
+        return f(pa._WINDOW_ARGS.pack(FAKE, query, FAKE, FAKE, FAKE, FAKE, FAKE, 0, 0, out_dtype, kv_dtype, T, mq, 4,
+                                      100, window, sinks, S, Hq, 8, D, 32, 16, scale))
+
+    for f in (lib.pa_decode_window_args, lib.pa_prefill_window_args):
+        f.argtypes = [ctypes.c_char_p]
+        for over, code in [(dict(window=0), -1), (dict(sinks=-1), -1), (dict(scale=0.0), -1), (dict(D=96), -2),
+                           (dict(Hq=24), -2), (dict(query=0), -1), (dict(out_dtype=9), -1), (dict(S=0), 0)]:
+            assert window(f, **over) == code
+    assert window(lib.pa_prefill_window_args, kv_dtype=0) == -2 and window(lib.pa_prefill_window_args, T=0) == 0
+    f = lib.pa_reshape_and_cache_rope_axes_args
+    f.argtypes = [ctypes.c_char_p]
+
+    def rope(freqs=FAKE, T=5, stride=8192, rope_dim=128, axes=3, halves=0, D=128):
+        return f(pa._ROPE_AXES_ARGS.pack(FAKE, FAKE + 64, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, freqs, FAKE, 0, 0, stride,
+                                         stride, stride, T, 32, 8, D, 16, 10, 2, rope_dim, axes, halves))
+
+    for over, code in [(dict(freqs=0), -1), (dict(stride=1), -1), (dict(rope_dim=130), -1), (dict(axes=0), -1),
+                       (dict(halves=2), -1), (dict(D=96), -2), (dict(T=0), 0)]:
+        assert rope(**over) == code
+
+
+def test_integers_past_32_bits_are_refused(pa):
+    with pytest.raises(pa.PAError) as e:
+        pa._send("x", None, pa._WINDOW_ARGS, *[0] * 15, 1 << 31, *[0] * 7, 0.5)
+    assert e.value.code == -1
+
+
 @pytest.mark.parametrize("over,why", [
     ({}, "CUDA device"),
     (dict(query=None), "go together"),
