@@ -51,7 +51,7 @@ namespace {
 constexpr int kThreads = 12 * 32;
 constexpr int kBM = 128, kBN = 64;  // rows of an item, keys of a tile
 constexpr float kGrowLog2 = 8.f;
-constexpr int kPlanSeqs = 255;       // sequences whose items are listed without gaps
+constexpr int kPlanSeqs = 2047;      // sequences whose items are listed without gaps
 
 struct Params {
     void *out;
@@ -266,26 +266,27 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     const int idx = (int)(item / (unsigned)p.num_kv_heads), g = (int)(item % (unsigned)p.num_kv_heads);
     int seq, unit;
     if (p.listed) {  // prefix sums of the sequences' units
-        int units = 0;
-        if (tid < p.num_seqs) {
-            const int q0 = p.query_start_loc[tid], q1 = p.query_start_loc[tid + 1];
-            int ctx;
-            if (sequence(p, q0, q1, p.context_lens[tid], blockIdx.x == 0, ctx))
-                units = min((q1 - q0 - 1) / (kBM >> p.group_log2) + 1, p.units_per_seq);
+        for (int i = tid; i <= p.num_seqs; i += kThreads) {
+            int units = 0, ctx;
+            if (i < p.num_seqs) {
+                const int q0 = p.query_start_loc[i], q1 = p.query_start_loc[i + 1];
+                if (sequence(p, q0, q1, p.context_lens[i], blockIdx.x == 0, ctx))
+                    units = min((q1 - q0 - 1) / (kBM >> p.group_log2) + 1, p.units_per_seq);
+            }
+            plan_mem[i] = units;
         }
-        if (tid < kPlanSeqs + 1) plan_mem[tid] = units;
         __syncthreads();
         if (warp == 0) {
             int carry = 0;
             for (int base = 0; base <= p.num_seqs; base += 32) {
-                const int i = base + lane, n = i <= kPlanSeqs ? plan_mem[i] : 0;
+                const int i = base + lane, n = i <= p.num_seqs ? plan_mem[i] : 0;
                 int v = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int w = __shfl_up_sync(kFullMask, v, o);
                     if (lane >= o) v += w;
                 }
-                if (i <= kPlanSeqs) plan_mem[i] = carry + v - n;
+                if (i <= p.num_seqs) plan_mem[i] = carry + v - n;
                 carry += __shfl_sync(kFullMask, v, 31);
             }
         }

@@ -214,6 +214,16 @@ def test_prefill_many_ragged_chunks(dtype, D):
     check(prefill, make_case(dtype, 8, 2, D, 8, ctx, 333, 7, chunks=chunks, seed=7), dtype, True)
 
 
+@pytest.mark.parametrize("S", [256, 384, 700, 2300])
+def test_prefill_many_sequences(S):
+    # single new tokens beside longer chunks: items listed without gaps, and past the list's length
+    rng = np.random.default_rng(S)
+    chunks = [int(x) for x in rng.integers(0, 3, S)]
+    chunks[1], chunks[S // 2], chunks[-1] = 70, 129, 33
+    ctx = [n + int(x) for n, x in zip(chunks, rng.integers(0, 60, S))]
+    check(prefill, make_case(BF16, 2, 1, 64, 8, ctx, 20, 3, chunks=chunks, seed=S), BF16, True)
+
+
 @pytest.mark.parametrize("D,bs,Hkv,G", [(128, 16, 1, 8), (64, 32, 2, 1), (128, 8, 2, 4)])
 @pytest.mark.parametrize("window,sinks", [(4096, 16), (700, 0), (1 << 30, 5)])
 def test_prefill_few_rows_behind_long_windows(D, bs, Hkv, G, window, sinks):
