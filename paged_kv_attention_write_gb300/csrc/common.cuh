@@ -193,6 +193,8 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), std::atomic<int> *ready
         const bool was_set = flag && flag->load(std::memory_order_acquire);
         if (!was_set) {
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            // clusters of 16 CTAs are past the size that every device has to offer
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
             if (flag) flag->store(1, std::memory_order_release);
         }

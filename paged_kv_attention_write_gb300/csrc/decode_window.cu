@@ -11,7 +11,8 @@
 // Keys are walked in groups of 8 consecutive tokens (the finest piece that one block of any
 // block size and one 128-byte-swizzled box holds), the groups of the sinks first, then
 // those of the window: "virtual" group v is logical group v below the sink groups and v +
-// shift above.  Only the groups at a border need a mask.
+// shift above.  Only the groups at a border need a mask.  A TMA box brings one group, or a
+// whole block where latency counts (both counts of groups then round to blocks).
 //
 // Per CTA one producer warp looks up block ids (one lane per group, a stage ahead) and
 // issues the TMA boxes into a ring of stages; the consumer warps each take their own groups
@@ -43,6 +44,7 @@ struct Params {
     const int32_t *block_tables, *context_lens;
     int max_blocks_per_seq, max_context_len, num_heads, num_kv_heads, group, block_size, num_blocks;
     int window, num_sinks;
+    int unit;  // groups of 8 keys that one TMA box brings: 1, or a block's
     float qk_scale_log2;
     int32_t *status;
 };
@@ -70,13 +72,14 @@ struct Keys {
     int ctx, lo, ns;         // visible: j < ctx and (j < ns or j >= lo)
     int sink_groups, shift;  // logical group of virtual group v: v, + shift from sink_groups on
     int groups;              // virtual groups
-    __device__ __forceinline__ Keys(int ctx_, int window, int num_sinks) : ctx(ctx_) {
+    __device__ __forceinline__ Keys(int ctx_, int window, int num_sinks, int unit) : ctx(ctx_) {
+        const int rows = 8 * unit;
         lo = max(0, ctx - window);
         ns = min(num_sinks, lo);
-        sink_groups = ns > 0 ? (ns - 1) / 8 + 1 : 0;
-        const int first = max(lo / 8, sink_groups);
+        sink_groups = ns > 0 ? ((ns - 1) / rows + 1) * unit : 0;
+        const int first = max(lo / rows * unit, sink_groups);
         shift = first - sink_groups;
-        groups = ctx > 0 ? sink_groups + (ctx - 1) / 8 + 1 - first : 0;
+        groups = ctx > 0 ? sink_groups + ((ctx - 1) / rows + 1) * unit - first : 0;
     }
     __device__ __forceinline__ int logical(int v) const { return v < sink_groups ? v : v + shift; }
     __device__ __forceinline__ bool sees(int j) const { return j < ctx && (j < ns || j >= lo); }
@@ -452,8 +455,10 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         if (threadIdx.x == 0 && rank == 0 && g == 0) report(p.status, PA_DEVERR_CONTEXT);
         ctx = ctx < 0 ? 0 : cap;
     }
-    const Keys keys(ctx, p.window, p.num_sinks);
-    const int v0 = (int)((int64_t)keys.groups * rank / CS), v1 = (int)((int64_t)keys.groups * (rank + 1) / CS);
+    const int unit = p.unit;
+    const Keys keys(ctx, p.window, p.num_sinks, unit);
+    const int64_t units = keys.groups / unit;
+    const int v0 = (int)(units * rank / CS) * unit, v1 = (int)(units * (rank + 1) / CS) * unit;
     const int stages = (v1 - v0 + NGRP - 1) / NGRP;
     volatile int *abort_v = abort_flag;
 
@@ -461,9 +466,10 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         // ============================================================ producer
         const int per_block = p.block_size / 8;
         const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
-        const bool is_v = lane >= NGRP;
-        const int slot = is_v ? lane - NGRP : lane;  // group of the stage
-        const bool mine = lane < 2 * NGRP;
+        const int per_stage = NGRP / unit;  // boxes of K, and of V
+        const bool is_v = lane >= per_stage, mine = lane < 2 * per_stage;
+        const int slot = (is_v ? lane - per_stage : lane) * unit;  // first group of the stage
+        const uint32_t box_bytes = Sh::GROUP_BYTES * unit;
         const uint64_t policy = policy_evict_first();
         auto group_of = [&](int i) { return keys.logical(v0 + i * NGRP + slot); };
         auto block_id = [&](int i) {
@@ -484,9 +490,10 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             const bool valid = in_range && id >= 0 && id < p.num_blocks;
             if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
             const unsigned boxes = __ballot_sync(kFullMask, valid);
+            const uint32_t groups = __reduce_or_sync(kFullMask, valid && !is_v ? ((1u << unit) - 1u) << slot : 0u);
             if (lane == 0) {
-                loaded[st] = boxes & ((1u << NGRP) - 1u);
-                mbar_arrive_expect_tx(full0 + 8 * st, __popc(boxes) * Sh::GROUP_BYTES);
+                loaded[st] = groups;
+                mbar_arrive_expect_tx(full0 + 8 * st, __popc(boxes) * box_bytes);
             }
             __syncwarp();
             if (valid) {
@@ -562,16 +569,37 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     const uint32_t a_o = smem_u32(sm_o), a_m = smem_u32(sm_m), a_l = smem_u32(sm_l);
     for (int i = i0 + (int)threadIdx.x; i < i1; i += Sh::THREADS) {
         const int h = i / (D / 2), d = i % (D / 2) * 2;
+        // eight CTAs' loads in flight together (a remote load takes a few hundred clocks)
         float M = -INFINITY, L = 0.f;
         float2 acc = make_float2(0.f, 0.f);
-        for (int r = 0; r < CS; ++r) M = fmaxf(M, ld_cluster(map_rank(a_m + 4 * h, r)));
-        for (int r = 0; r < CS; ++r) {
-            const float mr = ld_cluster(map_rank(a_m + 4 * h, r));
-            const float f = mr == -INFINITY ? 0.f : fast_exp2(mr - M);
-            L = fmaf(ld_cluster(map_rank(a_l + 4 * h, r)), f, L);
-            const float2 x = ld_cluster2(map_rank(a_o + 4 * (h * D + d), r));
-            acc.x = fmaf(x.x, f, acc.x);
-            acc.y = fmaf(x.y, f, acc.y);
+        for (int r0 = 0; r0 < CS; r0 += 8) {
+            float mr[8], lr[8];
+            float2 xr[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int from = min(r0 + r, CS - 1);
+                mr[r] = ld_cluster(map_rank(a_m + 4 * h, from));
+                lr[r] = ld_cluster(map_rank(a_l + 4 * h, from));
+                xr[r] = ld_cluster2(map_rank(a_o + 4 * (h * D + d), from));
+            }
+            float top = M;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                if (r0 + r >= CS) mr[r] = -INFINITY;
+                top = fmaxf(top, mr[r]);
+            }
+            const float keep = M == -INFINITY ? 0.f : fast_exp2(M - top);
+            M = top;
+            L *= keep;
+            acc.x *= keep;
+            acc.y *= keep;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const float f = mr[r] == -INFINITY ? 0.f : fast_exp2(mr[r] - M);
+                L = fmaf(lr[r], f, L);
+                acc.x = fmaf(xr[r].x, f, acc.x);
+                acc.y = fmaf(xr[r].y, f, acc.y);
+            }
         }
         const float inv = L > 0.f ? 1.f / L : 0.f;
         store_pair(p.out, p.out_dtype, ((int64_t)s * p.num_heads + g * heads + h) * D + d, acc.x * inv, acc.y * inv);
@@ -624,27 +652,34 @@ int launch_decode_window(const DecodeArgs &a) {
     p.status = a.status;
     const int64_t rows = (int64_t)a.num_blocks * a.block_size;
     if (rows <= 0 || rows > INT32_MAX) return PA_ERR_INVALID_ARG;
-    CUtensorMap km, vm;
-    for (int i = 0; i < 2; ++i) {
-        CUtensorMap *m = i ? &vm : &km;
-        const void *base = i ? a.value_cache : a.key_cache;
-        const int rc = a.kv_dtype == PA_F32
-                           ? make_kv_tensor_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 1, 8)
-                           : make_kv_block_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 8);
-        if (rc != PA_OK) return rc;
-    }
-    // The cluster size: the CTAs of one full wave, but none with less than one stage of keys.
-    // A CTA past the first wave costs more than its shorter run of keys gives back, and
-    // clusters start slowly: 256 (sequence, kv head) pairs of 1028 keys took 23, 29, 40 and
-    // 61 us in clusters of 1, 2, 4 and 8; 61 pairs of 790 keys 11.8, 8.6, 7.0 and 11.0 us;
-    // 8 pairs of 516 keys 11.1, 8.2, 6.5 and 5.9 us (bf16).
+    // The cluster size: the CTAs of one full wave, but none with less than one stage of keys
+    // (two past eight CTAs).  A CTA past the first wave costs more than its shorter run of keys
+    // gives back, and clusters start slowly: 256 (sequence, kv head) pairs of 1028 keys took 23,
+    // 29, 40 and 61 us in clusters of 1, 2, 4 and 8; 61 pairs of 790 keys 11.8, 8.6, 7.0 and
+    // 11.0 us; 8 pairs of 516 keys 11.1, 8.2, 6.5, 5.4 and (16) 5.7 us, of 4100 keys (8) 9.5 and
+    // (16) 7.7 us (bf16).
     const int sms = std::max(1, device_sm_count());
     const int64_t slots = (int64_t)sms * (a.kv_dtype == PA_F32 ? 1 : 2);  // resident CTAs
     const int64_t most = std::min<int64_t>(a.max_context_len, (int64_t)a.window + a.num_sinks);  // keys of a row
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
     const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads;
     int cluster = 1;
-    while (cluster < 8 && pairs * cluster * 2 <= slots && most > stage_keys * cluster) cluster *= 2;
+    while (cluster < 16 && pairs * cluster * 2 <= slots && most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
+        cluster *= 2;
+    // A box of a whole block where one warp's issue of the boxes bounds a CTA (about 70 clocks
+    // each: 8 pairs of 4100 keys 9.0 -> 7.7 us) or where the rows past the borders that it brings
+    // along are few (1024 pairs of 4112 keys in blocks of 16, 333 -> 318 us; but 256 pairs of 1028
+    // keys in blocks of 32, 23.3 -> 24.0 us).
+    p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
+    CUtensorMap km, vm;
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap *m = i ? &vm : &km;
+        const void *base = i ? a.value_cache : a.key_cache;
+        const int rc = a.kv_dtype == PA_F32
+                           ? make_kv_tensor_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 1, 8 * p.unit)
+                           : make_kv_block_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 8 * p.unit);
+        if (rc != PA_OK) return rc;
+    }
     switch (a.kv_dtype) {
         case PA_F32:
             return a.head_dim == 64 ? launch_f32<64>(p, cluster, a.num_seqs, km, vm, a.stream)

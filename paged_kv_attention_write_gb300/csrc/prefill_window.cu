@@ -653,17 +653,36 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             if (tok >= it.Lq) continue;
             float M = -INFINITY, L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int r = 0; r < cs; ++r) M = fmaxf(M, ld_cluster(map_rank(a_m + 4 * row, r)));
-            for (int r = 0; r < cs; ++r) {
-                const float m = ld_cluster(map_rank(a_m + 4 * row, r));
-                if (m == -INFINITY) continue;  // nothing seen (or no tile: no output there)
-                const float f = fast_exp2(m - M);
-                L = fmaf(ld_cluster(map_rank(a_l + 4 * row, r)), f, L);
-                const float4 x = ld_cluster4(map_rank(a_o + 4 * (row * Sh::PITCH + d), r));
-                acc.x = fmaf(x.x, f, acc.x);
-                acc.y = fmaf(x.y, f, acc.y);
-                acc.z = fmaf(x.z, f, acc.z);
-                acc.w = fmaf(x.w, f, acc.w);
+            for (int r0 = 0; r0 < cs; r0 += 4) {  // four CTAs' loads in flight together
+                float mr[4], lr[4];
+                float4 xr[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int from = min(r0 + r, cs - 1);
+                    mr[r] = ld_cluster(map_rank(a_m + 4 * row, from));
+                    lr[r] = ld_cluster(map_rank(a_l + 4 * row, from));
+                    xr[r] = ld_cluster4(map_rank(a_o + 4 * (row * Sh::PITCH + d), from));
+                }
+                float top = M;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (r0 + r >= cs) mr[r] = -INFINITY;
+                    top = fmaxf(top, mr[r]);
+                }
+                const float keep = M == -INFINITY ? 0.f : fast_exp2(M - top);
+                M = top;
+                L *= keep;
+                acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    if (mr[r] == -INFINITY) continue;  // nothing seen (or no tile: no output there)
+                    const float f = fast_exp2(mr[r] - M);
+                    L = fmaf(lr[r], f, L);
+                    acc.x = fmaf(xr[r].x, f, acc.x);
+                    acc.y = fmaf(xr[r].y, f, acc.y);
+                    acc.z = fmaf(xr[r].z, f, acc.z);
+                    acc.w = fmaf(xr[r].w, f, acc.w);
+                }
             }
             const float inv = L > 0.f ? 1.f / L : 0.f;
             const int64_t at =
@@ -739,7 +758,7 @@ int launch_prefill_window(const PrefillArgs &a) {
     // twos, 12.6 in fours.
     const int64_t keys = std::min<int64_t>(a.max_context_len, (int64_t)a.window + kBM / G + a.num_sinks);
     int cluster = 1;
-    while (cluster < 8 && items * cluster * 2 <= device_sm_count() && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
+    while (cluster < 16 && items * cluster * 2 <= device_sm_count() && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
     const int64_t rows = (int64_t)a.num_blocks * a.block_size;
     if (rows <= 0 || rows > INT32_MAX || items > INT32_MAX) return PA_ERR_INVALID_ARG;
     // Q boxes are 64 elements (the swizzle span) wide and cover the G heads of one kv head for
