@@ -93,7 +93,7 @@ def kernel_source_hash(kind: str = "decode") -> str:
     ncu counters to a kernel version)."""
     csrc = ROOT / "paged_kv_attention_write_gb300" / "csrc"
     files = {"decode": ["decode_kernels.cuh", "decode.cu", "tma.cuh", "common.cuh"],
-             "prefill": ["prefill.cu", "tma.cuh", "common.cuh"]}[kind]
+             "prefill": ["prefill.cu", "tcgen05.cuh", "tma.cuh", "common.cuh"]}[kind]
     h = hashlib.sha256()
     for f in files:
         h.update(_code_only((csrc / f).read_text()).encode())

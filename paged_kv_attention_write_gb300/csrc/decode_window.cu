@@ -25,6 +25,10 @@
 //     weights keep 16 bits or more and the output the accuracy of fp32 weights.
 //   fp32 caches: packed fp32 FMAs, eight lanes per key, four keys per warp step, at most
 //     four query heads per warp.
+// Measured (bf16 or fp16, D 128, GPU us): 128 sequences x 4112 keys, 64 q / 8 kv heads 313
+// (6.85 TB/s, the measured copy rate is 6.68); 32 x 1028, 32 / 8 heads 23.0 (5.7 TB/s: 256 CTAs
+// of 17 stages, the first loads and the last merges show); 1 x 516 5.5, 1 x 4100 7.7 (launch,
+// a chain of context -> block table -> box -> scores -> joins).
 // Every mbarrier wait is bounded in time.
 #include <algorithm>
 #include <type_traits>

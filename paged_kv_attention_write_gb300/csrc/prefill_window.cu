@@ -25,15 +25,18 @@
 // (maximum, sum, output) of the rows through distributed shared memory.
 //
 // Measured (us; 8 chunks of 512 tokens, 64 q / 8 kv heads, window 4096, fp16 | 4 chunks of
-// 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window 301): this 498 | 40 |
-// 28; the same with persistent CTAs 507 | 45 | 28; one CTA per SM with 128-key tiles and three
-// S buffers, as the causal kernel has, 545 | 47 | 42; two CTAs with 128-key tiles and one S
-// buffer each 555 | 57 | 40, with S issued for two 64-key tiles at once 574 | 53 | 30; two row
-// tiles per CTA taking turns, eight softmax warps each, 582 | 67 | 53.  What bounds it: with no
-// exponentials, no maxima and no P stores (a timing-only build) the first case still took 469
-// us.  An S product of 64 keys occupies the tensor core for 48 clocks, not 32 (it reads 16
-// columns of all of Q, 4 KB, for 2 KB of K), and four issuers' batches queue behind each other
-// while each tile waits S -> softmax -> P.V with two tiles in flight per CTA.
+// 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window 301): this 460 | 38 |
+// 25 (1200, 575 and 155 TFLOP/s).  Steps tried on the way, each in its own build: persistent
+// CTAs 507 | 45 | 28; one CTA per SM with 128-key tiles and three S buffers, as the causal
+// kernel has, 545 | 47 | 42; two CTAs with 128-key tiles and one S buffer each 555 | 57 | 40,
+// with S issued for two 64-key tiles at once 574 | 53 | 30; two row tiles per CTA taking turns,
+// eight softmax warps each, 582 | 67 | 53.
+// What bounds it: a tile takes its CTA about 1550 clocks, nearly all of them in the softmax
+// warps (TMEM load, maxima, exponentials, P store, hand-over), and 8 to 9 thousand clocks of an
+// item are its beginning and end; the tensor core is busy 52 % of the time and its queue 76 %
+// (an S product of 64 keys occupies it for 48 clocks, not 32: it reads 16 columns of all of Q,
+// 4 KB, for 2 KB of K).  With no exponentials, no maxima and no P stores (a timing-only build
+// of the 507 us step) 469 us were left; with no K and V loads at all, 427 of 500.
 //
 // Warps: 0 TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the rows
 // of V that no row of the item looks at, so that stale or NaN slots never meet a zero
