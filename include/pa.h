@@ -338,7 +338,9 @@ int pa_decode_rope(void *out, pa_dtype out_dtype, const void *query, const void 
  *    sequence sees: the blocks behind the window may have been freed, their entries hold
  *    anything (-1, say).  What the cache holds in slots that no row of the sequence sees is
  *    never used, not even NaN;
- *  - there is no workspace: the pieces of a split context are merged inside the launch.
+ *  - there is no workspace: the pieces of a split context are merged inside the launch.  A
+ *    call may be captured into a CUDA graph after one eager call with its types, head
+ *    dimension and head grouping on the device.
  * window < 1, num_sinks < 0 or scale <= 0 returns PA_ERR_INVALID_ARG.
  */
 

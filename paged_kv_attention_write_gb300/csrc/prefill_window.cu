@@ -197,7 +197,7 @@ __device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int 
     it.q0 = q0;
     it.Lq = q1 - q0;
     it.tok = unit * tt;
-    if (!ok || it.tok >= it.Lq) return false;
+    if (!ok || unit < 0 || it.tok >= it.Lq) return false;
     it.first = ctx - it.Lq + it.tok;
     it.last = ctx - it.Lq + min(it.Lq, it.tok + tt) - 1;
     it.lo = max(0, it.first - p.window + 1);
@@ -716,6 +716,17 @@ template <class T, int D>
 int launch_typed(const Params &p, int64_t items, int cluster, const CUtensorMap &qm, const CUtensorMap &km,
                  const CUtensorMap &vm, cudaStream_t st) {
     static std::atomic<int> whole_ready[kMaxDevices], split_ready[kMaxDevices];  // shared-memory limit raised
+    // Both kernels are loaded by a device's first call, so that a captured call of other sizes
+    // than the eager ones before it loads nothing.
+    static std::atomic<int> loaded[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices || !loaded[dev].load(std::memory_order_acquire)) {
+        for (auto kernel : {prefill_window_kernel<T, D, false>, prefill_window_kernel<T, D, true>})
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D>::SMEM) != cudaSuccess)
+                return PA_ERR_CUDA;
+        if (dev >= 0 && dev < kMaxDevices) loaded[dev].store(1, std::memory_order_release);
+    }
     const dim3 grid((unsigned)(items * cluster)), block(kThreads);
     const cudaError_t e = cluster > 1 ? launch_pdl_cluster(prefill_window_kernel<T, D, true>, split_ready, grid, block,
                                                            Shape<D>::SMEM, cluster, st, qm, km, vm, p)
@@ -756,12 +767,13 @@ int launch_prefill_window(const PrefillArgs &a) {
     p.listed = a.num_seqs <= kPlanSeqs && most < uniform;
     const int64_t items = (p.listed ? most : uniform) * a.num_kv_heads;
     // Few items: a cluster of CTAs takes each, up to one CTA per SM and at least four key tiles
-    // per CTA (joining costs about two tiles' time).  45 rows of 8 heads behind 4096 keys: 45.0
-    // us whole, 15.0 us in eights; 45 rows of 32 heads behind 512 keys: 11.7 whole, 10.8 in
-    // twos, 12.6 in fours.
+    // per CTA (the join costs about one tile's time).  45 rows of 8 heads behind 4096 keys: 45.0
+    // us whole, 13.9 in eights, 12.8 in sixteens; of 32 heads behind 512 keys: 11.7 whole, 9.6
+    // in twos.
     const int64_t keys = std::min<int64_t>(a.max_context_len, (int64_t)a.window + kBM / G + a.num_sinks);
+    const int sms = device_sm_count();
     int cluster = 1;
-    while (cluster < 16 && items * cluster * 2 <= device_sm_count() && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
+    while (cluster < 16 && items * cluster * 2 <= sms && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
     const int64_t rows = (int64_t)a.num_blocks * a.block_size;
     if (rows <= 0 || rows > INT32_MAX || items > INT32_MAX) return PA_ERR_INVALID_ARG;
     // Q boxes are 64 elements (the swizzle span) wide and cover the G heads of one kv head for

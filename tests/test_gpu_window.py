@@ -72,6 +72,15 @@ def test_decode_long_contexts_and_batches(dtype, S, window, D):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("bs,window,sinks", [(16, 1040, 20), (16, 1023, 1), (32, 2048, 33)])
+def test_decode_large_batches_behind_wide_windows(dtype, bs, window, sinks):
+    # more (sequence, kv head) pairs than CTAs fit at once: no clusters, whole-block boxes
+    rng = np.random.default_rng(window)
+    ctx = [int(c) for c in rng.integers(0, window + 700, 40)] + [window, window + sinks, window + bs - 1, 1]
+    check(decode, make_case(dtype, 8, 8, 64, bs, ctx, window, sinks, seed=bs + sinks), FP32)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
 def test_decode_large_scores_and_ties(dtype):
     # keys that dwarf the others, all keys alike, and a sink that takes nearly all of the weight
     case = make_case(dtype, 8, 2, 64, 16, [50, 300, 301], 40, 3, seed=5)
@@ -379,3 +388,46 @@ def test_a_stream_of_steps(sections, halves):
                     # sqrt(2 D) products of size 1: under 6 deviations), weights once more
                     e_score = 6 * 2.0 ** -8 * np.sqrt(2 * D) * D ** -0.5
                     assert (np.abs(out[r, h].double().cpu().numpy() - want) <= 2 * (e_score + 2.0 ** -8) * mag).all()
+
+
+def test_beside_the_causal_kernels_on_another_stream():
+    """Windowed and causal calls at once: they share the SMs' tensor memory."""
+    import paged_kv_attention_write_gb300 as pa
+    case = make_case(BF16, 32, 8, 128, 16, [900, 700, 300, 1200], 256, 4, chunks=[300, 200, 64, 1], seed=40)
+    full = make_case(BF16, 32, 8, 128, 16, [900, 700, 300, 1200], 1 << 20, 0, chunks=[300, 200, 64, 1], seed=41)
+    t, f = case.cuda(), full.cuda()
+    want = prefill(case, t=t)
+    chunk = torch.empty_like(want)
+
+    def causal(out, stream):
+        pa.pa_prefill_chunk(out, f["query"], f["starts"], full.max_query, f["key_cache"], f["value_cache"], f["tables"],
+                            f["ctx"], full.max_ctx, full.scale, stream=stream)
+
+    causal(chunk, None)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    a, b = torch.empty_like(want), torch.empty_like(chunk)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(50):
+        prefill(case, t=t, out=a, stream=s1, status=status)
+        causal(b, s2)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and torch.equal(a, want) and torch.equal(b, chunk)
+
+
+def test_a_captured_call_of_other_sizes_than_the_eager_ones():
+    # split items (a cluster) captured after an eager call with whole ones, and the other way round
+    small = make_case(BF16, 8, 2, 128, 16, [3000], 2048, 4, chunks=[40], seed=50)
+    large = make_case(BF16, 32, 8, 128, 16, [500, 900], 100, 4, chunks=[400, 700], seed=51)
+    for eager, captured in ((large, small), (small, large)):
+        te, tc = eager.cuda(), captured.cuda()
+        prefill(eager, t=te)
+        out = torch.zeros(tuple(captured.query.shape), device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            prefill(captured, out=out, t=tc)
+        g.replay()
+        torch.cuda.synchronize()
+        assert_close(out, captured, FP32, True)
