@@ -276,15 +276,18 @@ int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
                       int window, int num_sinks, int num_seqs, int num_heads, int num_kv_heads,
                       int head_dim, int block_size, int num_blocks, float scale, pa_dtype kv_dtype,
                       int32_t *status, pa_stream_t stream) {
+    // no rows: nothing is read, and empty tensors have no address
+    const bool nothing = num_tokens == 0 || max_query_len == 0;
     int rc = check_attention(out, out_dtype, query, key_cache, value_cache, block_tables,
-                             max_blocks_per_seq, context_lens, max_context_len, num_seqs,
+                             max_blocks_per_seq, context_lens, max_context_len,
+                             nothing && num_seqs > 0 ? 0 : num_seqs,
                              num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                              kv_dtype);
     if (rc != PA_OK) return rc;
     if (kv_dtype == PA_F32) return PA_ERR_UNSUPPORTED;
     if (num_tokens < 0 || max_query_len < 0 || window < 1 || num_sinks < 0 || !(scale > 0.f))
         return PA_ERR_INVALID_ARG;
-    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return PA_OK;
+    if (num_seqs == 0 || nothing) return PA_OK;
     if (!query_start_loc || !aligned(query_start_loc, 4) || !aligned(status, 4))
         return PA_ERR_INVALID_ARG;
     pa::PrefillArgs a{out,          out_dtype,  query,        query_start_loc,   num_tokens,

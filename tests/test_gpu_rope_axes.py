@@ -171,3 +171,29 @@ def test_streams_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(bits(b["kc"]), bits(want_k))
+
+
+def test_empty_steps_and_padding_alone():
+    import paged_kv_attention_write_gb300 as pa
+    b = build(BF16, 6, 4, 2, 64, 8, [20, 12], False, seed=8)
+    run(b, True)
+    slots, pos, rope = b["_keep"]
+    none = torch.empty((0, 4, 64), dtype=BF16, device="cuda")
+    kv = torch.empty((0, 2, 64), dtype=BF16, device="cuda")
+    pa.pa_reshape_and_cache_rope_axes(none.clone(), none, kv, kv.clone(), b["kc"], b["vc"], slots[:0], pos[:, :0].contiguous(),
+                                      rope)
+    b["slots"][:] = -3
+    for pool in (b["kc"], b["vc"]):
+        pool.fill_(float("nan"))
+    assert_rotated(run(b, True), b["q"], b, True)
+    assert b["kc"].isnan().all() and b["vc"].isnan().all()
+
+
+def test_misaligned_rows_are_refused():
+    import paged_kv_attention_write_gb300 as pa
+    b = build(BF16, 6, 4, 2, 64, 8, [20, 12], False, seed=9)
+    wide = torch.zeros((6, 4 * 64 + 4), dtype=BF16, device="cuda")
+    for q in (wide[:, 4:].view(6, 4, 64), wide[:, :256].view(6, 4, 64)):   # pointer, then stride
+        with pytest.raises(pa.PAError) as e:
+            run({**b, "q": q}, True)
+        assert e.value.code == -1

@@ -431,3 +431,99 @@ def test_a_captured_call_of_other_sizes_than_the_eager_ones():
         g.replay()
         torch.cuda.synchronize()
         assert_close(out, captured, FP32, True)
+
+
+@pytest.mark.parametrize("run,rounded,chunks,dtypes", [
+    (decode, False, None, (BF16, FP16, FP32)),
+    (prefill, True, [100, 1, 300, 40], (BF16, FP16)),     # items of one CTA
+    (prefill, True, [3, 1, 20, 9], (BF16,)),              # items split over a cluster
+])
+@pytest.mark.parametrize("window,sinks", [(1 << 20, 0), (700, 8)])
+def test_scores_that_grow_along_the_keys(run, rounded, chunks, dtypes, window, sinks):
+    # the running maximum keeps moving, by more than 2^8 between tiles: every rescaling of what
+    # has been summed so far is taken
+    for dtype in dtypes:
+        case = make_case(dtype, 8, 2, 128, 16, [1500, 90, 2100, 700], window, sinks, chunks=chunks, seed=60)
+        case.query *= 4
+        for s in range(4):
+            for b, blk in enumerate(case.tables[s].tolist()):
+                if blk >= 0:
+                    case.key_cache[blk] *= 0.25 + 4.0 * b / case.tables.shape[1]
+        out = run(case, FP32)
+        ref, mag = reference(case)
+        # queries four times and keys up to 4.25 times larger than bound() assumes; the rounding of
+        # weights does not depend on the scores
+        e = 17 * bound(case, ref, mag, FP32, False) + (bound(case, ref, mag, FP32, True) if rounded else 0)
+        got = out.double().cpu().numpy()
+        assert np.isfinite(got).all() and (np.abs(got - ref) <= e).all()
+
+
+@pytest.mark.parametrize("out_dtype", [BF16, FP16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=NAMES.get)
+def test_output_types(dtype, out_dtype):
+    case = make_case(dtype, 8, 2, 64, 16, [50, 300, 0, 129], 100, 5, seed=61)
+    check(decode, case, out_dtype)
+    if dtype != FP32:
+        for chunks in ([50, 200, 0, 65], [2, 5, 0, 1]):
+            check(prefill, make_case(dtype, 8, 2, 64, 16, [50, 900, 0, 600], 400, 5, chunks=chunks, seed=62), out_dtype, True)
+
+
+def test_empty_calls_and_misaligned_tensors():
+    import paged_kv_attention_write_gb300 as pa
+    case = make_case(BF16, 8, 2, 64, 16, [50, 300], 100, 5, seed=63)
+    t = case.cuda()
+    none = {k: t[k][:0] for k in ("query", "tables", "ctx")}
+    out = torch.empty((0, 8, 64), device="cuda")
+    pa.pa_decode_window(out, none["query"], t["key_cache"], t["value_cache"], none["tables"], none["ctx"], 0, 100, 5, 0.1)
+    pa.pa_prefill_window(out, none["query"], t["starts"][:1], 0, t["key_cache"], t["value_cache"], none["tables"],
+                         none["ctx"], 0, 100, 5, 0.1)
+    # sequences that all have no rows in this step
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    pa.pa_prefill_window(out, none["query"], zero, 0, t["key_cache"], t["value_cache"], t["tables"], t["ctx"], 300, 100,
+                         5, 0.1)
+    off = torch.empty(2 * 8 * 64 + 1, dtype=BF16, device="cuda")[1:].view(2, 8, 64)
+    for kw in (dict(out=off), dict(t={**t, "query": off})):
+        with pytest.raises(pa.PAError) as e:
+            decode(case, BF16, **kw)
+        assert e.value.code == -1
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+def test_decode_thousands_of_sequences(dtype):
+    rng = np.random.default_rng(64)
+    ctx = [int(c) for c in rng.integers(0, 70, 3000)]
+    check(decode, make_case(dtype, 2, 1, 64, 8, ctx, 30, 2, seed=64), FP32)
+
+
+def test_many_kv_heads():
+    case = make_case(BF16, 96, 24, 64, 8, [33, 200, 77], 50, 3, seed=65)
+    check(decode, case, FP32)
+    check(prefill, make_case(BF16, 96, 24, 64, 8, [33, 200, 77], 50, 3, chunks=[33, 70, 2], seed=66), FP32, True)
+
+
+def test_host_threads_call_at_once():
+    import threading
+    cases = [make_case(dt, 8, 2, D, 16, [400, 90], 128, 4, chunks=[60, 7], seed=70 + i)
+             for i, (dt, D) in enumerate([(BF16, 64), (FP16, 64), (BF16, 128), (FP16, 128)])]
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            t = cases[i].cuda()
+            torch.cuda.synchronize()
+            for _ in range(10):
+                got[i] = prefill(cases[i], t=t, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for case, out in zip(cases, got):
+        assert_close(out, case, FP32, True)

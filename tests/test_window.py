@@ -112,6 +112,8 @@ def test_windowed_calls_with_nothing_to_do(lib):
     assert _decode(lib, S=0, query=None, out=None) == 0
     assert _prefill(lib, S=0, query=None) == 0
     assert _prefill(lib, T=0, qsl=None) == 0
+    assert _prefill(lib, T=0, out=None, query=None) == 0 and _prefill(lib, mq=0, out=None, query=None) == 0
+    assert _prefill(lib, T=0, S=-1) == _prefill(lib, T=0, window=0) == -1
 
 
 def _prefill(lib, **over):
