@@ -412,7 +412,8 @@ int pa_rope_pair_axes(int32_t *pair_axis, int rope_dim, const int32_t *sections,
  *              the token's query is rotated all the same)
  *
  * Strides are in elements, at least the row and a multiple of 16 bytes (so the three may be
- * slices of one projection's output).  num_heads = 0 (query and query_out NULL) rotates and
+ * slices of one projection's output).  query_out and the caches overlap no other tensor of
+ * the call, query_out == query apart.  num_heads = 0 (query and query_out NULL) rotates and
  * writes keys only.  Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i], the
  * angle formed exactly and reduced to [-pi, pi] in fp32 (positions below 2^24 in magnitude),
  * rotation in fp32, rounded once; elements past rope_dim and values are bit copies.  A

@@ -7,11 +7,11 @@ the C++ scheduler writes the whole batch description into one pinned host buffer
 (``pa_engine_upload``), and one more call (``pa_engine_attend``) enqueues the step's
 copy-on-write block copies, the fresh K/V written into the paged cache and decode or
 chunked-prefill attention, reading the batch from that copy (``pa_engine_attend_window`` when
-the engine is made with a sliding window).  The model side is supplied by the caller: ``qkv(step)`` returns the device tensors q ``[T][Hq][D]``, k and
-v ``[T][Hkv][D]`` of the step's query tokens (``step`` holds their token ids and positions, on
-the host and, through ``device_tokens``, on the device), ``sample(step, out)`` returns one next
-token per sequence.  Marshalling only: every computation on the data runs in the library's
-kernels.
+the engine is made with a sliding window).  The model side is supplied by the caller:
+``qkv(step)`` returns the device tensors q ``[T][Hq][D]``, k and v ``[T][Hkv][D]`` of the step's
+query tokens (``step`` holds their token ids and positions, on the host and, through
+``device_tokens``, on the device), ``sample(step, out)`` returns one next token per sequence.
+Marshalling only: every computation on the data runs in the library's kernels.
 """
 from __future__ import annotations
 
@@ -57,7 +57,8 @@ class PagedAttentionEngine:
                  prefix_cache: bool = True, scale: Optional[float] = None, window: Optional[int] = None,
                  num_sinks: int = 0):
         """``window``: attend the newest ``window`` keys and the first ``num_sinks`` only."""
-        if (window is not None and window < 1) or num_sinks < 0 or (num_sinks and window is None):
+        if (window is not None and not 1 <= window < 2 ** 31) or not 0 <= num_sinks < 2 ** 31 or (
+                num_sinks and window is None):  # 32 bits: ctypes would cut off what is above
             raise ValueError("window is at least 1, num_sinks at least 0 and only with a window")
         self.window, self.num_sinks = window, num_sinks
         self.sched = Scheduler(num_blocks, block_size, token_budget, chunk_tokens, max_decode_steps,

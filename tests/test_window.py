@@ -229,6 +229,13 @@ def test_integers_past_32_bits_are_refused(pa):
     assert e.value.code == -1
 
 
+@pytest.mark.parametrize("kw", [dict(window=(1 << 32) + 5), dict(window=1 << 31), dict(window=5, num_sinks=1 << 32)])
+def test_engine_refuses_windows_past_32_bits(pa, kw):
+    from paged_kv_attention_write_gb300.engine import PagedAttentionEngine
+    with pytest.raises(ValueError):
+        PagedAttentionEngine(8, 8, 8, 2, 128, **kw)
+
+
 @pytest.mark.parametrize("over,why", [
     ({}, "CUDA device"),
     (dict(query=None), "go together"),
