@@ -25,6 +25,10 @@
 //     weights keep 16 bits or more and the output the accuracy of fp32 weights.
 //   fp32 caches: packed fp32 FMAs, eight lanes per key, four keys per warp step, at most
 //     four query heads per warp.
+// Many (sequence, kv head) pairs of few keys each (16-bit caches; the rule is at the launch)
+// take one warp, a CTA of its own, per pair instead: it issues its own boxes into its own ring
+// and joins nothing.  In the clusters' kernel such pairs wait for the start and the end of a
+// CTA of five warps, two of them at a time on an SM; here up to eight pairs are in flight.
 // Measured (bf16 or fp16, D 128, GPU us): 128 sequences x 4112 keys, 64 q / 8 kv heads 313
 // (6.85 TB/s, the measured copy rate is 6.68); 32 x 1028, 32 / 8 heads 23.0 (5.7 TB/s: 256 CTAs
 // of 17 stages, the first loads and the last merges show); 1 x 516 5.5, 1 x 4100 7.7 (launch,
@@ -611,6 +615,97 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     cluster_sync();  // nobody leaves while its shared memory is read
 }
 
+// One warp per (sequence, kv head): block b takes pair b (sequence-major).  The ring's `depth`
+// steps hold two groups of K and two of V each; the warp refills a step when it has read it.
+template <class T, int D>
+__global__ void __launch_bounds__(32)
+decode_window_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                          const Params p, int depth) {
+    using Sh = Shape<T, D>;
+    constexpr int GB = Sh::GROUP_BYTES, STEP = 4 * GB;
+    static_assert(Sh::HW * (Sh::PITCH + 2) * 4 <= STEP, "the result fits one step");
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t ring = smem_u32(smem), full0 = ring + depth * STEP;
+    const int lane = threadIdx.x;
+    if (lane == 0) {
+        for (int i = 0; i < depth; ++i) mbar_init(full0 + 8 * i, 1);
+        fence_barrier_init();
+        prefetch_tensormap(&kmap);
+        prefetch_tensormap(&vmap);
+    }
+    __syncwarp();
+    pdl_wait_previous();
+    pdl_launch_dependents();
+
+    const int s = blockIdx.x / (unsigned)p.num_kv_heads, g = blockIdx.x % (unsigned)p.num_kv_heads;
+    const int cap = min(p.max_blocks_per_seq * p.block_size, p.max_context_len);
+    int ctx = p.context_lens[s];
+    if (ctx < 0 || ctx > cap) {
+        if (lane == 0 && g == 0) report(p.status, PA_DEVERR_CONTEXT);
+        ctx = ctx < 0 ? 0 : cap;
+    }
+    const int unit = p.unit;  // 1 or 2
+    const Keys keys(ctx, p.window, p.num_sinks, unit);
+    const int steps = (keys.groups + 1) / 2, per_block = p.block_size / 8, k_boxes = 2 / unit;
+    const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
+    auto block_id = [&](int v) { return v < keys.groups ? bt[keys.logical(v) / per_block] : -1; };
+    // block ids of 32 groups, one per lane, and of the next 32
+    int ids = block_id(lane), ids_next = block_id(32 + lane);
+    Consumer16<T, D> work(p, 0, lane, s, g);
+    const uint64_t policy = policy_evict_first();
+    uint32_t loaded = 0;  // two bits per step of the ring: its valid groups
+    auto issue = [&](int t, int slot) {
+        if (t > 0 && t % 16 == 0) {
+            ids = ids_next;
+            ids_next = block_id(2 * t + 32 + lane);
+        }
+        const int v = 2 * t + (unit == 1 ? lane & 1 : 0), id = __shfl_sync(kFullMask, ids, v & 31);
+        const bool in_range = lane < 2 * k_boxes && v < keys.groups;
+        const bool valid = in_range && id >= 0 && id < p.num_blocks;
+        if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
+        const unsigned boxes = __ballot_sync(kFullMask, valid);
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * slot, __popc(boxes) * GB * unit);
+        __syncwarp();
+        if (valid) {
+            const int at = id * per_block + (keys.logical(v) & (per_block - 1));  // group of 8 rows of the pool
+            tma_load_5d(ring + slot * STEP + lane * GB * unit, lane < k_boxes ? &kmap : &vmap, 0, 0, 0, at, g,
+                        full0 + 8 * slot, policy);
+        }
+        __syncwarp();
+        loaded = (loaded & ~(3u << 2 * slot)) | (unit == 1 ? boxes & 3u : boxes & 1u ? 3u : 0u) << 2 * slot;
+    };
+    for (int t = 0; t < depth && t < steps; ++t) issue(t, t);
+    int slot = 0, phase = 0;
+    for (int t = 0; t < steps; ++t) {
+        if (!__all_sync(kFullMask, mbar_wait(full0 + 8 * slot, phase, p.status))) break;
+        const uint32_t kb = ring + slot * STEP, valid = loaded >> 2 * slot & 3u;
+        const bool wrote = valid && work.pair(p, keys, kb, kb + 2 * GB, 2 * t, valid);
+        if (t + depth < steps) {
+            // rows zeroed here are written by TMA (the async proxy) next
+            if (wrote) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            issue(t + depth, slot);
+        }
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+    // the heads' rows through shared memory, so that the stores are contiguous
+    __syncwarp();
+    float *red_o = reinterpret_cast<float *>(smem), *red_m = red_o + Sh::HW * Sh::PITCH, *red_l = red_m + Sh::HW;
+    work.finish(red_o, red_m, red_l);
+    __syncwarp();
+    for (int i = lane; i < p.group * (D / 2); i += 32) {
+        const int h = i / (D / 2), d = i % (D / 2) * 2;
+        const float L = red_l[h], inv = L > 0.f ? 1.f / L : 0.f;
+        const float2 x = *reinterpret_cast<const float2 *>(red_o + h * Sh::PITCH + d);
+        store_pair(p.out, p.out_dtype, ((int64_t)s * p.num_heads + g * p.group + h) * D + d, x.x * inv, x.y * inv);
+    }
+}
+
 template <class T, int D, int G>
 int launch_typed(const Params &p, int cluster, int num_seqs, const CUtensorMap &km, const CUtensorMap &vm,
                  cudaStream_t st) {
@@ -620,6 +715,38 @@ int launch_typed(const Params &p, int cluster, int num_seqs, const CUtensorMap &
                               dim3(Sh::THREADS), Sh::SMEM, cluster, st, km, vm, p) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+// 16-bit caches: clusters, or (`warps` > 0) a warp per pair, so many of them on an SM; at most 8,
+// which leaves a ring three steps or more.
+template <class T, int D>
+int launch_16(const Params &p, int cluster, int num_seqs, int warps, const CUtensorMap &km, const CUtensorMap &vm,
+              cudaStream_t st) {
+    constexpr int STEP = 4 * Shape<T, D>::GROUP_BYTES, kMost = 16, kRest = 1024 + 8 * kMost;
+    static_assert((228 * 1024 / 8 - 1024 - kRest) / STEP >= 3, "eight warps fit an SM");
+    // A device's first call loads both kernels, with the shared memory that any call asks for: a
+    // later one may be captured, whichever kernel it takes.
+    static std::atomic<int> clusters_ready[kMaxDevices], warps_ready[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    if (dev < 0 || dev >= kMaxDevices || !warps_ready[dev].load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(decode_window_kernel<T, D, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Shape<T, D>::SMEM) != cudaSuccess ||
+            cudaFuncSetAttribute(decode_window_warp_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMost * STEP + kRest) != cudaSuccess)
+            return PA_ERR_CUDA;
+        if (dev >= 0 && dev < kMaxDevices) warps_ready[dev].store(1, std::memory_order_release);
+    }
+    cudaError_t e;
+    if (warps > 0) {
+        const int depth = std::min(kMost, (228 * 1024 / warps - 1024 - kRest) / STEP);  // 1 KB per CTA is the system's
+        e = launch_pdl_cluster(decode_window_warp_kernel<T, D>, warps_ready, dim3(p.num_kv_heads * num_seqs), dim3(32),
+                               depth * STEP + kRest, 1, st, km, vm, p, depth);
+    } else {
+        e = launch_pdl_cluster(decode_window_kernel<T, D, 0>, clusters_ready, dim3(cluster, p.num_kv_heads, num_seqs),
+                               dim3(Shape<T, D>::THREADS), Shape<T, D>::SMEM, cluster, st, km, vm, p);
+    }
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <int D>
@@ -675,6 +802,16 @@ int launch_decode_window(const DecodeArgs &a) {
     // along are few (1024 pairs of 4112 keys in blocks of 16, 333 -> 318 us; but 256 pairs of 1028
     // keys in blocks of 32, 23.3 -> 24.0 us).
     p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
+    // A warp per pair where the clusters would be single CTAs in more than one wave, of rows of
+    // about a thousand keys at most: 1024 pairs of 132, 516 and 1028 keys 29.8 -> 16.4, 59.7 -> 47.3
+    // and 95.5 -> 87.7 us, 320 pairs of 516 keys 27.2 -> 24.6 us.  Of 2052 keys the two are equal,
+    // of 4112 the clusters faster (318 and 332 us), and rows of unequal length leave the longest
+    // to one warp: contexts of 10 to 1000 keys 52.6 -> 50.8, of 10 to 2000 90.8 -> 99 us.  Boxes of
+    // 16 keys where the rows are long for the warps on an SM (320 pairs of 516 keys 26.3 -> 24.6,
+    // but 1024 pairs of 132 keys 16.4 -> 17.9 us).
+    const bool by_warp = a.kv_dtype != PA_F32 && pairs > slots && most <= 1152 && pairs <= INT32_MAX;
+    const int warps = by_warp ? (int)std::min<int64_t>(8, (pairs + sms - 1) / sms) : 0;  // on an SM
+    if (by_warp) p.unit = a.block_size >= 16 && most >= 128 * warps ? 2 : 1;
     CUtensorMap km, vm;
     for (int i = 0; i < 2; ++i) {
         CUtensorMap *m = i ? &vm : &km;
@@ -689,11 +826,11 @@ int launch_decode_window(const DecodeArgs &a) {
             return a.head_dim == 64 ? launch_f32<64>(p, cluster, a.num_seqs, km, vm, a.stream)
                                     : launch_f32<128>(p, cluster, a.num_seqs, km, vm, a.stream);
         case PA_F16:
-            return a.head_dim == 64 ? launch_typed<F16, 64, 0>(p, cluster, a.num_seqs, km, vm, a.stream)
-                                    : launch_typed<F16, 128, 0>(p, cluster, a.num_seqs, km, vm, a.stream);
+            return a.head_dim == 64 ? launch_16<F16, 64>(p, cluster, a.num_seqs, warps, km, vm, a.stream)
+                                    : launch_16<F16, 128>(p, cluster, a.num_seqs, warps, km, vm, a.stream);
         case PA_BF16:
-            return a.head_dim == 64 ? launch_typed<BF16, 64, 0>(p, cluster, a.num_seqs, km, vm, a.stream)
-                                    : launch_typed<BF16, 128, 0>(p, cluster, a.num_seqs, km, vm, a.stream);
+            return a.head_dim == 64 ? launch_16<BF16, 64>(p, cluster, a.num_seqs, warps, km, vm, a.stream)
+                                    : launch_16<BF16, 128>(p, cluster, a.num_seqs, warps, km, vm, a.stream);
     }
     return PA_ERR_UNSUPPORTED;
 }

@@ -495,6 +495,64 @@ def test_decode_thousands_of_sequences(dtype):
     check(decode, make_case(dtype, 2, 1, 64, 8, ctx, 30, 2, seed=64), FP32)
 
 
+# More (sequence, kv head) pairs than single CTAs fit at once, of short rows: one warp per pair.
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
+@pytest.mark.parametrize("Hkv,G", [(8, 8), (16, 1), (8, 4), (24, 2)])
+@pytest.mark.parametrize("D,bs", [(64, 8), (64, 16), (128, 16), (128, 32)])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (20, 3), (500, 13), (10 ** 6, 0)])
+def test_decode_many_short_rows(dtype, Hkv, G, D, bs, window, sinks):
+    rng = np.random.default_rng(Hkv * G + window % 91)
+    ctx = [0, 1, 2, 8, 9, 15, 16, 17, 19, 20, 21, 23, 24, 33, 500, 513, 514, 515, 700]
+    ctx += [int(c) for c in rng.integers(0, 700, 42 - len(ctx))]
+    case = make_case(dtype, Hkv * G, Hkv, D, bs, ctx, window, sinks, seed=Hkv + D + bs)
+    check(decode, case, FP32)
+    if window == 500:
+        check(decode, case, dtype)
+
+
+def test_decode_many_short_rows_report_bad_blocks_and_contexts():
+    ctx = [300, 301, 60, 310] + [40] * 156
+    case = make_case(BF16, 8, 2, 64, 8, ctx, 100, 4, seed=80)
+    t = case.cuda()
+    good = decode(case, t=t)
+    t["tables"][0, 30] = case.key_cache.shape[0]      # a block of the window
+    t["tables"][3, 0] = -5                            # the sinks' block
+    t["tables"][1, 10] = 1 << 30                      # behind the window: not read
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = decode(case, t=t, status=status)
+    assert status.item() == 2
+    keep = [i for i in range(160) if i not in (0, 3)]
+    assert torch.equal(out[keep], good[keep]) and torch.isfinite(out).all()
+    for bad, want in ((-7, 0), (2 ** 31 - 1, 310)):
+        t = case.cuda()
+        t["ctx"][3] = bad
+        status.zero_()
+        out = decode(case, t=t, status=status)
+        assert status.item() == 4
+        assert torch.equal(out[3], good[3] if want else torch.zeros_like(out[3]))
+        assert torch.equal(out[4:], good[4:])
+
+
+def test_decode_captured_with_another_kernel_than_the_eager_call():
+    small = make_case(BF16, 16, 8, 128, 16, [3000, 4], 900, 4, seed=81)
+    large = make_case(BF16, 16, 8, 128, 16, [60, 400] * 25, 300, 4, seed=82)
+    for eager, captured in ((large, small), (small, large)):
+        te, tc = eager.cuda(), captured.cuda()
+        decode(eager, t=te)
+        out = torch.zeros(tuple(captured.query.shape), device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            decode(captured, out=out, t=tc)
+            decode(captured, out=out, t=tc)
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert_close(out, captured, FP32, False)
+        assert torch.equal(out, decode(captured, t=tc))
+
+
 def test_many_kv_heads():
     case = make_case(BF16, 96, 24, 64, 8, [33, 200, 77], 50, 3, seed=65)
     check(decode, case, FP32)
