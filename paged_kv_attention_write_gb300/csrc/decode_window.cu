@@ -23,8 +23,8 @@
 //     rate (the kernel is bound by HBM), but on the CUDA cores eight heads would bound it.
 //     P enters as a rounded part plus its rounded remainder (two products), so that the
 //     weights keep 16 bits or more and the output the accuracy of fp32 weights.
-//   fp32 caches: packed fp32 FMAs, eight lanes per key, four keys per warp step, at most
-//     four query heads per warp.
+//   fp32 caches: packed fp32 FMAs, eight lanes per key, eight keys per warp step, at most four
+//     query heads per warp.
 // Many (sequence, kv head) pairs of few keys each (16-bit caches; the rule is at the launch)
 // take one warp, a CTA of its own, per pair instead: it issues its own boxes into its own ring
 // and joins nothing.  In the clusters' kernel such pairs wait for the start and the end of a
@@ -33,6 +33,9 @@
 // (6.85 TB/s, the measured copy rate is 6.68); 32 x 1028, 32 / 8 heads 23.0 (5.7 TB/s: 256 CTAs
 // of 17 stages, the first loads and the last merges show); 1 x 516 5.5, 1 x 4100 7.7 (launch,
 // a chain of context -> block table -> box -> scores -> joins).
+// fp32 caches, 64 sequences x 2052 keys, 8 kv heads, D 128: 155 (1 query head per kv head, 6.9
+// TB/s), 159 (4), 183 (8).  CTAs of eight consumer warps, one per SM, took 164, 171 and 210:
+// nothing ran under their beginnings and ends.
 // Every mbarrier wait is bounded in time.
 #include <algorithm>
 #include <type_traits>
@@ -63,8 +66,8 @@ struct Shape {
     static constexpr int GROUP_BYTES = 8 * D * T::kBytes;        // 8 tokens of one kv head
     static constexpr int NGRP = 16384 / GROUP_BYTES;             // groups per stage (16 KB of K, 16 KB of V)
     static constexpr int KV_BYTES = NGRP * GROUP_BYTES;
-    static constexpr int NSTAGE = kF32 ? 6 : 3;
-    static constexpr int NW = kF32 ? 8 : 4;                      // consumer warps
+    static constexpr int NSTAGE = 3;
+    static constexpr int NW = 4;                     // consumer warps
     static constexpr int THREADS = (NW + 1) * 32;
     static constexpr int HW = kF32 ? 4 : 8;                      // query heads a warp holds
     static constexpr int PITCH = D + 4;                          // floats between the merge buffer's head rows
@@ -303,29 +306,32 @@ struct Consumer16 {
     }
 };
 
-// fp32: lane = 8 * key of four + part; a part owns the 16-byte pieces part, part + 8, .. of a
-// row.  Each of the four lane groups keeps its own maximum; finish() joins them.
+// fp32: a warp takes a group of 8 keys at a time, lane = 8 * (key % 4) + part; a part owns the
+// 16-byte pieces part, part + 8, .. of a row.  The partial scores of a lane (two keys, HW heads)
+// are summed over the eight parts by halving: each exchange sends the half that the other lane
+// keeps, so that a lane ends with one whole score, key u = part / 4 of head own, and takes one
+// exponential (all lanes adding up all of their scores: 24 exchanges and 8 exponentials where
+// this takes 7 and 1).
 template <int D, int G>
 struct Consumer32 {
     using Sh = Shape<F32, D>;
     static constexpr int HW = G < 4 ? G : 4;     // query heads of this warp
     static constexpr int QS = G / HW;            // warps that share a key, on different heads
-    static constexpr int KW = Sh::NW / QS;       // warps over the keys of a stage
-    static constexpr int KEYS = Sh::NGRP * 8 / KW;
+    static constexpr int KW = Sh::NW / QS;       // warps over the groups of a stage
     static constexpr int NC = D / 32;            // 16-byte pieces per lane
-    static_assert(KEYS % 4 == 0 && KEYS >= 4, "whole steps of four keys");
     float2 q[HW][NC * 2], o[HW][NC * 2];
-    float m[HW], l[HW];
+    float m, l;  // of head own (l: this lane's keys; lanes that differ in idle bits of part hold the same)
     int warp, lane;
 
+    // part (below 4) whose lane holds head h
+    static __device__ __forceinline__ int part_of(int h) { return HW == 4 ? h : HW == 2 ? 2 * h : 0; }
+
     __device__ __forceinline__ Consumer32(const Params &p, int warp_, int lane_, int s, int g)
-        : warp(warp_), lane(lane_) {
+        : m(-INFINITY), l(0.f), warp(warp_), lane(lane_) {
         const float *qp = static_cast<const float *>(p.query) +
                           ((int64_t)s * p.num_heads + g * G + (warp % QS) * HW) * D + (lane & 7) * 4;
 #pragma unroll
         for (int h = 0; h < HW; ++h) {
-            m[h] = -INFINITY;
-            l[h] = 0.f;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const float4 x = *reinterpret_cast<const float4 *>(qp + h * D + c * 32);
@@ -345,49 +351,81 @@ struct Consumer32 {
         }
     }
 
+    // v[0 .. N) summed over the lanes that differ in bit `off`; each keeps N / 2 of them, the
+    // lanes with the bit set the upper ones (one value: both keep it).
+    template <int N>
+    __device__ __forceinline__ void halve(float (&v)[2 * HW], int off) {
+        if constexpr (N == 1) {
+            v[0] += __shfl_xor_sync(kFullMask, v[0], off);
+        } else {
+            const bool upper = (lane & off) != 0;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                const float send = upper ? v[i] : v[i + N / 2], keep = upper ? v[i + N / 2] : v[i];
+                v[i] = keep + __shfl_xor_sync(kFullMask, send, off);
+            }
+        }
+    }
+
     __device__ __forceinline__ bool stage(const Params &p, const Keys &keys, uint32_t kbase, uint32_t vbase, int first,
                                           uint32_t valid) {
 #pragma unroll 1
-        for (int i = 0; i < KEYS; i += 4) {
-            const int key = (warp / QS) * KEYS + i + (lane >> 3);  // of the stage
-            const bool seen = (valid >> (key / 8) & 1u) && keys.sees(8 * keys.logical(first + key / 8) + key % 8);
-            if (!__any_sync(kFullMask, seen)) continue;
-            float2 x[NC * 2];
-            row(kbase + key * D * 4 + (lane & 7) * 16, x);
-            float s[HW];
-            bool grow = false;
+        for (int gr = warp / QS; gr < Sh::NGRP; gr += KW) {
+            if (!(valid >> gr & 1u)) continue;
+            const int lg = keys.logical(first + gr), key = lane >> 3;  // keys `key` and `key` + 4 of the group
+            const bool whole = keys.sees_group(lg);
+            const uint32_t at = (gr * 8 + key) * D * 4 + (lane & 7) * 16;
+            float v[2 * HW];
 #pragma unroll
-            for (int h = 0; h < HW; ++h) {
-                float2 a = __fmul2_rn(q[h][0], x[0]);
-#pragma unroll
-                for (int c = 1; c < NC * 2; ++c) a = __ffma2_rn(q[h][c], x[c], a);
-                s[h] = a.x + a.y;
-#pragma unroll
-                for (int off = 1; off < 8; off <<= 1) s[h] += __shfl_xor_sync(kFullMask, s[h], off);
-                s[h] = seen ? s[h] : -INFINITY;
-                grow |= s[h] > m[h] + kGrowLog2;
-            }
-            if (__any_sync(kFullMask, grow)) {
+            for (int u = 0; u < 2; ++u) {
+                float2 x[NC * 2];
+                row(kbase + at + u * 4 * D * 4, x);
 #pragma unroll
                 for (int h = 0; h < HW; ++h) {
-                    const float mn = fmaxf(m[h], s[h]);
-                    const float a = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mn);
-                    m[h] = mn;
-                    l[h] *= a;
+                    float2 a = __fmul2_rn(q[h][0], x[0]);
 #pragma unroll
-                    for (int c = 0; c < NC * 2; ++c) o[h][c] = __fmul2_rn(o[h][c], make_float2(a, a));
+                    for (int c = 1; c < NC * 2; ++c) a = __ffma2_rn(q[h][c], x[c], a);
+                    v[u * HW + h] = a.x + a.y;
                 }
             }
-            row(vbase + key * D * 4 + (lane & 7) * 16, x);
+            halve<2 * HW>(v, 4);
+            halve<HW>(v, 2);
+            halve<(HW + 1) / 2>(v, 1);
+            float s = v[0];
+            if (!whole && !keys.sees(8 * lg + key + (lane & 4))) s = -INFINITY;
+            if (__any_sync(kFullMask, s > m + kGrowLog2)) {
+                float mx = s;
 #pragma unroll
-            for (int c = 0; c < NC * 2; ++c)  // no NaN times zero
-                if (!seen) x[c] = make_float2(0.f, 0.f);
+                for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFullMask, mx, off));
+                const float mn = fmaxf(m, mx);
+                const float f = m == -INFINITY ? 0.f : fast_exp2(m - mn);
+                m = mn;
+                l *= f;
 #pragma unroll
-            for (int h = 0; h < HW; ++h) {
-                const float w = m[h] == -INFINITY ? 0.f : fast_exp2(s[h] - m[h]);
-                l[h] += w;
+                for (int h = 0; h < HW; ++h) {
+                    const float fh = __shfl_sync(kFullMask, f, part_of(h));
 #pragma unroll
-                for (int c = 0; c < NC * 2; ++c) o[h][c] = __ffma2_rn(make_float2(w, w), x[c], o[h][c]);
+                    for (int c = 0; c < NC * 2; ++c) o[h][c] = __fmul2_rn(o[h][c], make_float2(fh, fh));
+                }
+            }
+            const float w = m == -INFINITY ? 0.f : fast_exp2(s - m);
+            l += w;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float2 x[NC * 2];
+                row(vbase + at + u * 4 * D * 4, x);
+                if (!whole) {  // no NaN times zero
+                    const bool seen = keys.sees(8 * lg + key + 4 * u);
+#pragma unroll
+                    for (int c = 0; c < NC * 2; ++c)
+                        if (!seen) x[c] = make_float2(0.f, 0.f);
+                }
+#pragma unroll
+                for (int h = 0; h < HW; ++h) {
+                    const float wh = __shfl_sync(kFullMask, w, (lane & 24) + 4 * u + part_of(h));
+#pragma unroll
+                    for (int c = 0; c < NC * 2; ++c) o[h][c] = __ffma2_rn(make_float2(wh, wh), x[c], o[h][c]);
+                }
             }
         }
         return false;
@@ -395,21 +433,16 @@ struct Consumer32 {
 
     __device__ __forceinline__ void finish(float *red_o, float *red_m, float *red_l) {
 #pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(kFullMask, l, off);
+#pragma unroll
         for (int h = 0; h < HW; ++h) {
-            float M = m[h];
-            M = fmaxf(M, __shfl_xor_sync(kFullMask, M, 8));
-            M = fmaxf(M, __shfl_xor_sync(kFullMask, M, 16));
-            const float a = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - M);
-            float L = l[h] * a;
-            L += __shfl_xor_sync(kFullMask, L, 8);
-            L += __shfl_xor_sync(kFullMask, L, 16);
-            if (lane == 0) {
-                red_m[h] = M;
-                red_l[h] = L;
+            if (lane == part_of(h)) {
+                red_m[h] = m;
+                red_l[h] = l;
             }
 #pragma unroll
             for (int c = 0; c < NC * 2; ++c) {
-                float2 v = __fmul2_rn(o[h][c], make_float2(a, a));
+                float2 v = o[h][c];
 #pragma unroll
                 for (int off = 8; off < 32; off <<= 1) {
                     v.x += __shfl_xor_sync(kFullMask, v.x, off);
@@ -425,7 +458,7 @@ struct Consumer32 {
 // grid = (cluster size, kv heads, sequences), cluster (cluster size, 1, 1).  G is the group
 // size for fp32 caches; 0 (any group up to 8) for 16-bit ones.
 template <class T, int D, int G>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS, Shape<T, D>::kF32 ? 1 : 2)
+__global__ void __launch_bounds__(Shape<T, D>::THREADS, 2)
 decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const Params p) {
     using Sh = Shape<T, D>;
@@ -790,12 +823,18 @@ int launch_decode_window(const DecodeArgs &a) {
     // 11.0 us; 8 pairs of 516 keys 11.1, 8.2, 6.5, 5.4 and (16) 5.7 us, of 4100 keys (8) 9.5 and
     // (16) 7.7 us (bf16).
     const int sms = std::max(1, device_sm_count());
-    const int64_t slots = (int64_t)sms * (a.kv_dtype == PA_F32 ? 1 : 2);  // resident CTAs
+    const int64_t slots = 2 * sms;  // resident CTAs
     const int64_t most = std::min<int64_t>(a.max_context_len, (int64_t)a.window + a.num_sinks);  // keys of a row
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
     const int64_t pairs = (int64_t)a.num_seqs * a.num_kv_heads;
+    // What is resident in clusters of a size, as the parts of the chip do not divide evenly: of
+    // 304 CTAs 296 in fours, 288 in eights, 224 in sixteens.  One cluster more is a second wave
+    // (76 pairs of 333 fp32 keys 6.0 us in twos, 9.1 in fours; 16 pairs of 2004 keys 7.4 in eights,
+    // 11.6 in sixteens).
+    auto fit = [&](int size) { return slots * (size <= 2 ? 64 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
     int cluster = 1;
-    while (cluster < 16 && pairs * cluster * 2 <= slots && most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
+    while (cluster < 16 && pairs * cluster * 2 <= fit(cluster * 2) &&
+           most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
         cluster *= 2;
     // A box of a whole block where one warp's issue of the boxes bounds a CTA (about 70 clocks
     // each: 8 pairs of 4100 keys 9.0 -> 7.7 us) or where the rows past the borders that it brings
