@@ -404,17 +404,21 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
     if (query is None) != (query_out is None):
         _refuse(what, "query and query_out go together")
     shape, ks = key.shape, key_cache.shape
-    if len(shape) != 3 or len(ks) != 4 or value.shape != shape or value_cache.shape != ks or shape[1:] != ks[2:]:
+    if len(shape) != 3 or len(ks) != 4 or value.shape != shape or value_cache.shape != ks:
         _refuse(what, "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
-    (T, Hkv, D), dt, dev = shape, key.dtype, key.get_device()
+    (T, Hkv, D), (NB, bs, ch, cd), dt, dev = shape, ks, key.dtype, key.get_device()
+    if Hkv != ch or D != cd:
+        _refuse(what, "key and value are [T][Hkv][D], a cache [NB][bs][Hkv][D]")
     one_device = (dev >= 0 and value.get_device() == dev == key_cache.get_device() == value_cache.get_device() ==
                   slot_mapping.get_device() == positions.get_device() == rope.freqs.get_device())
     Hq = q_stride = 0
     if query is not None:
         qs = query.shape
-        if len(qs) != 3 or query_out.shape != qs or qs[0] != T or qs[2] != D:
+        if len(qs) != 3 or query_out.shape != qs:
             _refuse(what, "query and query_out are [T][Hq][D]")
-        Hq = qs[1]
+        rows, Hq, width = qs
+        if rows != T or width != D:
+            _refuse(what, "query and query_out are [T][Hq][D]")
         q_stride, q_head, q_one = query.stride()
         if query.dtype is not dt or query_out.dtype is not dt:
             _refuse(what, "query, keys, values and caches share one dtype")
@@ -449,4 +453,4 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
         value.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), slot_mapping.data_ptr(), positions.data_ptr(),
         rope.freqs.data_ptr(), rope.pair_axis.data_ptr(), 0 if status is None else status.data_ptr(),
         _current_stream(dev) if stream is None else _stream(stream), q_stride, k_stride, v_stride, T, Hq, Hkv, D,
-        ks[1], ks[0], code, rope.rope_dim, rope.num_axes, rope.halves)
+        bs, NB, code, rope.rope_dim, rope.num_axes, rope.halves)
