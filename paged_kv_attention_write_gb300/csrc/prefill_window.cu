@@ -19,27 +19,33 @@
 // what does not overlap: an item's first loads, its last product, its output.  So two CTAs
 // share an SM, each with half of TMEM (two 64-column S buffers and O) and of the shared
 // memory, and one's tiles run under the other's beginning and end; every scheduler has four
-// softmax warps.  One item per CTA: the hardware hands them out as CTAs end (persistent CTAs
-// dealt four 512-token chunks out unevenly, 9 to 68 key tiles per SM).  With fewer items than
-// half the SMs a cluster of CTAs takes each, a run of its key tiles per CTA, and joins the
-// (maximum, sum, output) of the rows through distributed shared memory.
+// softmax warps.  The grid is one CTA per item, but a CTA whose loads near their end calls off
+// one that has not started (cluster launch control) and goes on with its item: Q, keys and the
+// first S of the next item are under way while the softmax warps finish this one, and the
+// hardware still hands items out as places become free.  Warp 0 finds the items and passes them
+// on through two slots in shared memory.  With fewer items than half the SMs a cluster of CTAs
+// takes each, a run of its key tiles per CTA, and joins the (maximum, sum, output) of the rows
+// through distributed shared memory.
 //
 // Measured (us; 8 chunks of 512 tokens, 64 q / 8 kv heads, window 4096, fp16 | 4 chunks of
-// 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window 301): this 460 | 38 |
-// 25 (1200, 575 and 155 TFLOP/s).  Steps tried on the way, each in its own build: persistent
-// CTAs 507 | 45 | 28; one CTA per SM with 128-key tiles and three S buffers, as the causal
-// kernel has, 545 | 47 | 42; two CTAs with 128-key tiles and one S buffer each 555 | 57 | 40,
-// with S issued for two 64-key tiles at once 574 | 53 | 30; two row tiles per CTA taking turns,
-// eight softmax warps each, 582 | 67 | 53.
+// 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window 301 | 16 fresh prompts
+// of 100 to 1500, 32 / 8, window 1024): this 455 | 34.9 | 23.2 | 153 (1213, 625, 168 TFLOP/s);
+// one item per CTA 460 | 37.6 | 23.3 | 188.  The loads of K and of V are one loop: as two copies
+// the warps' loops together miss the instruction cache (476 | 38.0).  Steps tried on the way,
+// each in its own build: CTAs that own every n-th item 507 | 45 | 28 (uneven, 9 to 68 key tiles
+// per SM); one CTA per SM with 128-key tiles and three S buffers, as the causal kernel has, 545 |
+// 47 | 42; two CTAs with 128-key tiles and one S buffer each 555 | 57 | 40, with S issued for two
+// 64-key tiles at once 574 | 53 | 30; two row tiles per CTA taking turns, eight softmax warps
+// each, 582 | 67 | 53.
 // What bounds it: a tile takes its CTA about 1550 clocks, nearly all of them in the softmax
-// warps (TMEM load, maxima, exponentials, P store, hand-over), and 8 to 9 thousand clocks of an
-// item are its beginning and end; the tensor core is busy 52 % of the time and its queue 76 %
-// (an S product of 64 keys occupies it for 48 clocks, not 32: it reads 16 columns of all of Q,
-// 4 KB, for 2 KB of K).  With no exponentials, no maxima and no P stores (a timing-only build
-// of the 507 us step) 469 us were left; with no K and V loads at all, 427 of 500.
+// warps (TMEM load, maxima, exponentials, P store, hand-over); the tensor core is busy 52 % of
+// the time and its queue 76 % (an S product of 64 keys occupies it for 48 clocks, not 32: it
+// reads 16 columns of all of Q, 4 KB, for 2 KB of K).  With no exponentials, no maxima and no P
+// stores (a timing-only build of the 507 us step) 469 us were left; with no K and V loads at
+// all, 427 of 500.
 //
-// Warps: 0 TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the rows
-// of V that no row of the item looks at, so that stale or NaN slots never meet a zero
+// Warps: 0 items, TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the
+// rows of V that no row of the item looks at, so that stale or NaN slots never meet a zero
 // weight), 4-11 softmax and output, each a 16-row slab through the 16-lane TMEM shapes.
 // Every mbarrier wait is bounded in time.
 #include <algorithm>
@@ -95,7 +101,7 @@ struct Shape {
     static constexpr int OFF_K = Q_BYTES;
     static constexpr int OFF_V = OFF_K + NK * KV_BYTES;
     static constexpr int OFF_BAR = OFF_V + NV * KV_BYTES;
-    static constexpr int SMEM = 1024 + OFF_BAR + 256 + 4 * (kPlanSeqs + 1);
+    static constexpr int SMEM = 1024 + OFF_BAR + 512 + 4 * (kPlanSeqs + 1);
     static_assert(2 * (SMEM + 1024) <= 228 * 1024, "two CTAs per SM");
     // split items: the CTA's output [128][PITCH] and its rows' maxima and sums, over Q and the rings
     static constexpr int PITCH = D + 8;              // floats (eight rows of a store on distinct banks)
@@ -215,6 +221,28 @@ __device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int 
     return true;
 }
 
+// Asks for the number of a CTA that has not started, which then never starts; the 16-byte answer
+// lands at `answer` and on the barrier.
+__device__ __forceinline__ void try_cancel(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     answer),
+                 "r"(bar)
+                 : "memory");
+}
+// false: every CTA has started
+__device__ __forceinline__ bool canceled(uint32_t answer, unsigned &number) {
+    uint32_t yes, x;
+    asm volatile(
+        "{\n\t.reg .b128 a;\n\t.reg .pred p;\n\tld.shared.b128 a, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+        : "=r"(yes), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    if (yes) number = x;
+    return yes != 0;
+}
+
 // SPLIT: a cluster of CTAs takes one item, each a run of its key tiles.
 template <class T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -244,16 +272,26 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     constexpr int BVF = BKE + NK;     // V stage landed
     constexpr int BVE = BVF + NV;     // P.V of that V finished
     constexpr int BTM = BVE + NV;     // TMEM allocated
-    constexpr int NBAR = BTM + 1;
+    constexpr int BQE = BTM + 1;      // S of an item finished: Q may be replaced
+    constexpr int BOE = BQE + 1;      // O of an item read
+    constexpr int BIF = BOE + 1;      // item slot written
+    constexpr int BIE = BIF + 2;      // item slot read by warps 1-11
+    constexpr int BCL = BIE + 2;      // answer to the request for another item
+    constexpr int NBAR = BCL + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     int *abort_flag = reinterpret_cast<int *>(bars + NBAR) + 1;
-    int *plan_mem = reinterpret_cast<int *>(smem + Sh::OFF_BAR + 256);
-    static_assert((NBAR + 1) * 8 <= 256, "barrier area");
+    constexpr int OFF_ANSWER = 352, OFF_ITEMS = 368;
+    Item *items = reinterpret_cast<Item *>(smem + Sh::OFF_BAR + OFF_ITEMS);  // [2]
+    int *plan_mem = reinterpret_cast<int *>(smem + Sh::OFF_BAR + 512);
+    static_assert((NBAR + 1) * 8 <= OFF_ANSWER && OFF_ITEMS + 2 * sizeof(Item) <= 512, "barrier area");
 
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         *abort_flag = 0;
-        for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i >= BPF && i < BPF + kSBufs ? 8 : 1);
+        for (int i = 0; i < NBAR; ++i) {
+            const bool softmax = (i >= BPF && i < BPF + kSBufs) || i == BOE;  // arrived on by those eight warps
+            mbar_init(bar(i), softmax ? 8 : i == BIE || i == BIE + 1 ? 11 : 1);
+        }
         fence_barrier_init();
         prefetch_tensormap(&qmap);
         prefetch_tensormap(&kmap);
@@ -265,15 +303,12 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     // CTAs are numbered sequence by sequence (the items of one share their keys in L2), from a
     // chunk's last rows to its first (the first rows of a fresh prompt see few keys), kv heads
     // side by side.
-    const unsigned item = SPLIT ? blockIdx.x / cluster_size() : blockIdx.x;
-    const int idx = (int)(item / (unsigned)p.num_kv_heads), g = (int)(item % (unsigned)p.num_kv_heads);
-    int seq, unit;
     if (p.listed) {  // prefix sums of the sequences' units
         for (int i = tid; i <= p.num_seqs; i += kThreads) {
             int units = 0, ctx;
             if (i < p.num_seqs) {
                 const int q0 = p.query_start_loc[i], q1 = p.query_start_loc[i + 1];
-                if (sequence(p, q0, q1, p.context_lens[i], blockIdx.x == 0, ctx))
+                if (sequence(p, q0, q1, p.context_lens[i], true, ctx))
                     units = min((q1 - q0 - 1) / (kBM >> p.group_log2) + 1, p.units_per_seq);
             }
             plan_mem[i] = units;
@@ -294,20 +329,29 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             }
         }
         __syncthreads();
-        const int u = plan_mem[p.num_seqs] - 1 - idx;
-        int lo = 0, hi = p.num_seqs;  // plan_mem[lo] <= u < plan_mem[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (plan_mem[mid] <= u) lo = mid; else hi = mid;
-        }
-        seq = lo;
-        unit = u < 0 ? INT32_MAX >> 8 : u - plan_mem[lo];  // past the last item: no such rows
-    } else {
-        seq = idx / p.units_per_seq;
-        unit = p.units_per_seq - 1 - idx % p.units_per_seq;
     }
+    // the item of a number; false when it has no rows
+    auto find = [&](unsigned number, bool rep, Item &it) {
+        const int idx = (int)(number / (unsigned)p.num_kv_heads), g = (int)(number % (unsigned)p.num_kv_heads);
+        int seq, unit;
+        if (p.listed) {
+            const int u = plan_mem[p.num_seqs] - 1 - idx;
+            int lo = 0, hi = p.num_seqs;  // plan_mem[lo] <= u < plan_mem[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (plan_mem[mid] <= u) lo = mid; else hi = mid;
+            }
+            seq = lo;
+            unit = u < 0 ? INT32_MAX >> 8 : u - plan_mem[lo];  // past the last item: no such rows
+        } else {
+            seq = idx / p.units_per_seq;
+            unit = p.units_per_seq - 1 - idx % p.units_per_seq;
+        }
+        return make_item(p, seq, unit, g, rep && !p.listed && unit == 0 && g == 0, it);
+    };
     Item it{};
-    const bool live = make_item(p, seq, unit, g, !p.listed && unit == 0 && g == 0 && tid == 0, it);
+    bool live = true;
+    if constexpr (SPLIT) live = find(blockIdx.x / cluster_size(), tid == 0, it);
     volatile int *abort_v = abort_flag;
     auto wait = [&](int b, uint32_t parity) {
         return mbar_try_wait(bar(b), parity & 1) || (!*abort_v && mbar_wait_idle(bar(b), parity & 1, p.status));
@@ -320,13 +364,31 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
         return got;
     };
-    // this CTA's key tiles: j0 + t, t < n
-    int j0 = 0, n = it.tiles;
+    // this CTA's key tiles of the item: j0 + t, t < n; `done` tiles of the items before
+    int j0 = 0, n = 0, done = 0;
     if constexpr (SPLIT) {
         const int cs = (int)cluster_size(), rank = (int)cluster_rank();
         j0 = (int)((int64_t)it.tiles * rank / cs);
         n = (int)((int64_t)it.tiles * (rank + 1) / cs) - j0;
     }
+    // The k-th item of this CTA, for warps 1-11: false after the last.
+    auto next_item = [&](int k) {
+        if constexpr (SPLIT) return k == 0;
+        done += n;
+        if (!__all_sync(kFullMask, wait(BIF + (k & 1), k >> 1))) {
+            *abort_v = 1;
+            return false;
+        }
+        if (warp >= 4) {  // softmax warps look the item up when they need it, and let it go at its end
+            n = items[k & 1].tiles;
+            return n > 0;
+        }
+        it = items[k & 1];
+        n = it.tiles;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BIE + (k & 1)));
+        return n > 0;
+    };
     bool ok = true;
 
     if (!live) {
@@ -341,39 +403,92 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         const uint64_t policy = policy_evict_normal();
         const int bl = p.block_log2, nb = kBN >> bl;  // blocks per key tile (2, 4 or 8)
         const uint32_t box_bytes = (uint32_t)(D * 2) << bl;
-        const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
-        const int sink_blocks = it.sk >> bl, shift = it.sh >> bl;
-        auto block_id = [&](int j) {
-            const int v = (j0 + j) * nb + lane;
-            return lane < nb && v < it.blocks ? bt[v < sink_blocks ? v : v + shift] : -1;
-        };
-        int id0 = block_id(0), id1 = block_id(1);
-        if (is_k && lane == 0) {
-            mbar_arrive_expect_tx(bar(BQF), Sh::Q_BYTES);
-            for (int hf = 0; hf < Sh::HALVES; ++hf)
-                tma_load_3d(sQ + hf * (kBM * 128), &qmap, hf * 64, it.g << p.group_log2, it.q0 + it.tok, bar(BQF),
-                            policy);
-        }
-        for (int t = 0; ok && t < n; ++t) {
-            const int id = id0;
-            id0 = id1;
-            id1 = block_id(t + 2);
-            const bool in_range = lane < nb && (j0 + t) * nb + lane < it.blocks;
-            const bool valid = in_range && id >= 0 && id < p.num_blocks;
-            if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
-            const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
-            const int st = t % NS;
-            int w_ok = 1;
+        // Warp 0 also finds the items.  The next one is asked of the hardware while this one's last
+        // tiles run: a CTA that has not started yet is called off and its number taken.
+        const uint32_t answer = sQ + Sh::OFF_BAR + OFF_ANSWER;
+        unsigned number = blockIdx.x;
+        int asked = 0, heard = 0;
+        auto ask = [&] {
             if (lane == 0) {
-                w_ok = wait(empty + st, t / NS + 1);
-                if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
+                fence_async_smem();  // the last answer has been read
+                mbar_arrive_expect_tx(bar(BCL), 16);
+                try_cancel(answer, bar(BCL));
             }
-            ok = __shfl_sync(kFullMask, w_ok, 0);
-            if (ok && valid)
-                tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
-                            bar(full + st), policy);
-            __syncwarp();
+            ++asked;
+        };
+        for (int k = 0; ok; ++k) {
+            if (SPLIT || !is_k) {
+                if (!next_item(k)) break;
+            } else {
+                bool more = true;  // the next item that has rows, if there is one
+                done += n;
+                n = 0;
+                while (ok && more) {
+                    if (asked > heard) {
+                        ok = __all_sync(kFullMask, wait(BCL, heard++));
+                        more = ok && canceled(answer, number);
+                        __syncwarp();
+                    }
+                    if (more && find(number, lane == 0, it)) {
+                        n = it.tiles;
+                        break;
+                    }
+                    if (more) ask();
+                }
+                ok = ok && __all_sync(kFullMask, wait(BIE + (k & 1), (k >> 1) + 1));
+                if (!ok) break;
+                if (lane == 0) {
+                    it.tiles = n;
+                    items[k & 1] = it;
+                    mbar_arrive(bar(BIF + (k & 1)));
+                }
+                __syncwarp();
+                if (n == 0) break;
+            }
+            const int32_t *bt = p.block_tables + (int64_t)it.s * p.max_blocks_per_seq;
+            const int sink_blocks = it.sk >> bl, shift = it.sh >> bl;
+            auto block_id = [&](int j) {
+                const int v = (j0 + j) * nb + lane;
+                return lane < nb && v < it.blocks ? bt[v < sink_blocks ? v : v + shift] : -1;
+            };
+            int id0 = block_id(0), id1 = block_id(1);
+            if (is_k) {
+                int w_ok = 1;
+                if (lane == 0) {
+                    w_ok = SPLIT || wait(BQE, k + 1);
+                    if (w_ok) {
+                        mbar_arrive_expect_tx(bar(BQF), Sh::Q_BYTES);
+                        for (int hf = 0; hf < Sh::HALVES; ++hf)
+                            tma_load_3d(sQ + hf * (kBM * 128), &qmap, hf * 64, it.g << p.group_log2, it.q0 + it.tok,
+                                        bar(BQF), policy);
+                    }
+                }
+                ok = __shfl_sync(kFullMask, w_ok, 0);
+            }
+#pragma unroll 1
+            for (int t = 0; ok && t < n; ++t) {
+                const int id = id0;
+                id0 = id1;
+                id1 = block_id(t + 2);
+                const bool in_range = lane < nb && (j0 + t) * nb + lane < it.blocks;
+                const bool valid = in_range && id >= 0 && id < p.num_blocks;
+                if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
+                const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
+                const int st = (done + t) % NS;
+                int w_ok = 1;
+                if (lane == 0) {
+                    w_ok = wait(empty + st, (done + t) / NS + 1);
+                    if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
+                }
+                ok = __shfl_sync(kFullMask, w_ok, 0);
+                if (ok && valid)
+                    tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
+                                bar(full + st), policy);
+                __syncwarp();
+                if (!SPLIT && is_k && t == n - 1) ask();
+            }
         }
+        if (!SPLIT && asked > heard) mbar_wait(bar(BCL), heard & 1, p.status);  // no answer is left to land
         if (!ok) *abort_v = 1;
     } else if (warp == 1) {
         // ============================================ S_t = Q K_t^T
@@ -385,58 +500,64 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-            mbar_arrive(bar(BTM));
-            ok = wait(BQF, 0);
-            for (int t = 0; ok && t < n; ++t) {
-                const int st = t % NK, sb = t % kSBufs;
-                ok = wait(BKF + st, t / NK) && wait(BPV + sb, t / kSBufs + 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sK = sQ + Sh::OFF_K + st * Sh::KV_BYTES;
+        if (lane == 0) mbar_arrive(bar(BTM));
+        for (int k = 0; ok && next_item(k); ++k) {
+            if (lane == 0) {
+                ok = wait(BQF, k);
+                for (int t = 0; ok && t < n; ++t) {
+                    const int st = (done + t) % NK, sb = (done + t) % kSBufs;
+                    ok = wait(BKF + st, (done + t) / NK) && wait(BPV + sb, (done + t) / kSBufs + 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sK = sQ + Sh::OFF_K + st * Sh::KV_BYTES;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_f16(tmem + sb * kBN, smem_desc(sQ + (k / 4) * (kBM * 128) + (k % 4) * 32, 16, 1024),
-                            smem_desc(sK + (k / 4) * 1024 + (k % 4) * 32, 16, Sh::GSTR), IDESC_S, k > 0);
-                mma_commit(bar(BSF + sb));
-                mma_commit(bar(BKE + st));
+                    for (int c = 0; c < D / 16; ++c)
+                        mma_f16(tmem + sb * kBN, smem_desc(sQ + (c / 4) * (kBM * 128) + (c % 4) * 32, 16, 1024),
+                                smem_desc(sK + (c / 4) * 1024 + (c % 4) * 32, 16, Sh::GSTR), IDESC_S, c > 0);
+                    mma_commit(bar(BSF + sb));
+                    mma_commit(bar(BKE + st));
+                }
+                if (!SPLIT && ok) mma_commit(bar(BQE));
             }
-            if (!ok) *abort_v = 1;
+            ok = __shfl_sync(kFullMask, (int)ok, 0);
         }
+        if (!ok) *abort_v = 1;
     } else if (warp == 3) {
         // ============================================ O += P_t V_t, P from TMEM
         ok = wait_tmem();
-        for (int t = 0; ok && t < n; ++t) {
-            const int st = t % NV, pb = t % kSBufs, k0 = (j0 + t) * kBN;
-            const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
-            ok = __all_sync(kFullMask, wait(BVF + st, t / NV));
-            if (ok && (j0 + t < it.low || j0 + t >= it.high)) {
-                // rows of V that no row of the item sees: [ns, lo) and past the last row
-                const int gap0 = it.ns - k0, gap1 = it.virt(it.lo) - k0, end = it.last + 1 - it.sh - k0;
-                constexpr int VEC = Sh::HALVES * 8;  // 16-byte pieces of a row
-                if (gap1 > 0 || end < kBN)
-                    for (int i = lane; i < kBN * VEC; i += 32) {
-                        const int r = i / VEC, rest = i % VEC;
-                        if (r < end && (r < gap0 || r >= gap1)) continue;
-                        sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
-                               0u, 0u);
-                    }
-                fence_async_smem();
-                __syncwarp();
-            }
-            if (lane == 0) {
-                ok = ok && wait(BPF + pb, t / kSBufs);
-                if (ok) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < kBN / 16; ++k)
-                        mma_f16_tmem_a(tmem + kTmemO, tmem + pb * kBN + k * 8,
-                                       smem_desc(sV + k * 2 * Sh::GSTR, 1024, Sh::GSTR), IDESC_PV, t > 0 || k > 0);
-                    mma_commit(bar(BPV + pb));
-                    mma_commit(bar(BVE + st));
+        for (int k = 0; ok && next_item(k); ++k) {
+            for (int t = 0; ok && t < n; ++t) {
+                const int st = (done + t) % NV, pb = (done + t) % kSBufs, k0 = (j0 + t) * kBN;
+                const uint32_t sV = sQ + Sh::OFF_V + st * Sh::KV_BYTES;
+                ok = __all_sync(kFullMask, wait(BVF + st, (done + t) / NV));
+                if (ok && (j0 + t < it.low || j0 + t >= it.high)) {
+                    // rows of V that no row of the item sees: [ns, lo) and past the last row
+                    const int gap0 = it.ns - k0, gap1 = it.virt(it.lo) - k0, end = it.last + 1 - it.sh - k0;
+                    constexpr int VEC = Sh::HALVES * 8;  // 16-byte pieces of a row
+                    if (gap1 > 0 || end < kBN)
+                        for (int i = lane; i < kBN * VEC; i += 32) {
+                            const int r = i / VEC, rest = i % VEC;
+                            if (r < end && (r < gap0 || r >= gap1)) continue;
+                            sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
+                                   0u, 0u);
+                        }
+                    fence_async_smem();
+                    __syncwarp();
                 }
+                if (lane == 0) {
+                    ok = ok && (SPLIT || t > 0 || wait(BOE, k + 1)) && wait(BPF + pb, (done + t) / kSBufs);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < kBN / 16; ++c)
+                            mma_f16_tmem_a(tmem + kTmemO, tmem + pb * kBN + c * 8,
+                                           smem_desc(sV + c * 2 * Sh::GSTR, 1024, Sh::GSTR), IDESC_PV, t > 0 || c > 0);
+                        mma_commit(bar(BPV + pb));
+                        mma_commit(bar(BVE + st));
+                    }
+                }
+                ok = __shfl_sync(kFullMask, (int)ok, 0);
             }
-            ok = __shfl_sync(kFullMask, (int)ok, 0);
         }
         if (!ok) *abort_v = 1;
     } else {
@@ -452,194 +573,207 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         ok = wait_tmem();
         const uint32_t tL = tmem + ((uint32_t)lane0 << 16), tO = tL + kTmemO;
         const float sc = p.qk_scale_log2;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
-        for (int t = 0; ok && t < n; ++t) {
-            const int sb = t % kSBufs;
-            ok = __all_sync(kFullMask, wait(BSF + sb, t / kSBufs));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t tS = tL + sb * kBN;
-            uint32_t s[32];
-            tmem_ld_16x256b<8>(tS, s);
-            tmem_wait_ld();
-            if (j0 + t < it.low || j0 + t >= it.high) {
-                // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
-                // chunk (a ragged last item) as its last row: computed, never stored
-                const int k0 = (j0 + t) * kBN, ns = it.virt(p.num_sinks) - k0;
-                const int p0 = min(it.first + (row0 >> p.group_log2), it.last);
-                const int p1 = min(it.first + (row1 >> p.group_log2), it.last);
-                const int hi0 = it.virt(p0) - k0, lo0 = it.virt(max(0, p0 - p.window + 1)) - k0;
-                const int hi1 = it.virt(p1) - k0, lo1 = it.virt(max(0, p1 - p.window + 1)) - k0;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = 8 * i + 2 * ga + e;
-                        if (key > hi0 || (key < lo0 && key >= ns)) s[4 * i + e] = __float_as_uint(-INFINITY);
-                        if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
-                    }
-            }
-            // maximum of the 16 scores per row in this lane
-            float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                a0 = fmax3(a0, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
-                c0 = fmax3(c0, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
-                a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
-                c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
-            }
-            float mx0 = fmaxf(a0, c0) * sc, mx1 = fmaxf(a1, c1) * sc;
-            if (__any_sync(kFullMask, mx0 > m0 + kGrowLog2 || mx1 > m1 + kGrowLog2)) {
-                // the row's maximum, the same in its four lanes
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2));
-                const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
-                const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
-                const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
-                const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
-                l0 *= f0;
-                l1 *= f1;
-                m0 = n0;
-                m1 = n1;
-                if (t > 0) {  // O holds the tiles before: wait for the last P.V, scale the rows
-                    ok = __all_sync(kFullMask, wait(BPV + (t - 1) % kSBufs, (t - 1) / kSBufs));
-                    if (ok) {
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[16];
-                            tmem_ld_16x256b_x4(tO + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f0);
-                                o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f0);
-                                o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f1);
-                                o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f1);
-                            }
-                            tmem_st_16x256b_x4(tO + c, o);
-                        }
-                        tmem_wait_st();
-                    }
-                }
-            }
-            {
-                const float b0_ = m0 == -INFINITY ? 0.f : m0, b1_ = m1 == -INFINITY ? 0.f : m1;
-                const float2 sc2 = make_float2(sc, sc), n0 = make_float2(-b0_, -b0_), n1 = make_float2(-b1_, -b1_);
-                float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
-                uint32_t w[16];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
-                                                 sc2, n0);
-                    const float2 x1 = __ffma2_rn(
-                        make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
-                    w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
-                    w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
-                    add_pair<T>(r0, w[2 * i]);
-                    add_pair<T>(r1, w[2 * i + 1]);
-                }
-                if (ok) {
-                    tmem_st_16x128b_x8(tS, w);
-                    tmem_wait_st();
-                }
-                l0 += r0.x + r0.y;
-                l1 += r1.x + r1.y;
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (!ok) break;
-            if (lane == 0) mbar_arrive(bar(BPF + sb));
-        }
-        // ---- output
-        ok = ok && (n == 0 || __all_sync(kFullMask, wait(BPV + (n - 1) % kSBufs, (n - 1) / kSBufs)));
-        float L0 = l0 + __shfl_xor_sync(kFullMask, l0, 1), L1 = l1 + __shfl_xor_sync(kFullMask, l1, 1);
-        L0 += __shfl_xor_sync(kFullMask, L0, 2);
-        L1 += __shfl_xor_sync(kFullMask, L1, 2);
-        if constexpr (SPLIT) {
-            // into shared memory, over Q and the rings: every product that reads them is done
-            if (ga == 0) {
-                float *ml = reinterpret_cast<float *>(smem + Sh::OFF_M);
-                ml[row0] = m0;
-                ml[row1] = m1;
-                ml[kBM + row0] = L0;
-                ml[kBM + row1] = L1;
-            }
-            if (ok && n > 0) {
+        for (int k = 0; ok && next_item(k); ++k) {
+            const Item &cur = SPLIT ? it : items[k & 1];
+            const int low = cur.low, high = cur.high;
+            float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
+            for (int t = 0; ok && t < n; ++t) {
+                const int sb = (done + t) % kSBufs;
+                ok = __all_sync(kFullMask, wait(BSF + sb, (done + t) / kSBufs));
+                if (!ok) break;
                 tc_fence_after();
-                float *o = reinterpret_cast<float *>(smem);
+                const uint32_t tS = tL + sb * kBN;
+                uint32_t s[32];
+                tmem_ld_16x256b<8>(tS, s);
+                tmem_wait_ld();
+                if (j0 + t < low || j0 + t >= high) {
+                    // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
+                    // chunk (a ragged last item) as its last row: computed, never stored
+                    const int k0 = (j0 + t) * kBN, ns = cur.virt(p.num_sinks) - k0;
+                    const int p0 = min(cur.first + (row0 >> p.group_log2), cur.last);
+                    const int p1 = min(cur.first + (row1 >> p.group_log2), cur.last);
+                    const int hi0 = cur.virt(p0) - k0, lo0 = cur.virt(max(0, p0 - p.window + 1)) - k0;
+                    const int hi1 = cur.virt(p1) - k0, lo1 = cur.virt(max(0, p1 - p.window + 1)) - k0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int key = 8 * i + 2 * ga + e;
+                            if (key > hi0 || (key < lo0 && key >= ns)) s[4 * i + e] = __float_as_uint(-INFINITY);
+                            if (key > hi1 || (key < lo1 && key >= ns)) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
+                        }
+                }
+                // maximum of the 16 scores per row in this lane
+                float a0 = -INFINITY, a1 = -INFINITY, c0 = -INFINITY, c1 = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    a0 = fmax3(a0, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                    c0 = fmax3(c0, __uint_as_float(s[4 * i + 4]), __uint_as_float(s[4 * i + 5]));
+                    a1 = fmax3(a1, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+                    c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
+                }
+                float mx0 = fmaxf(a0, c0) * sc, mx1 = fmaxf(a1, c1) * sc;
+                if (__any_sync(kFullMask, mx0 > m0 + kGrowLog2 || mx1 > m1 + kGrowLog2)) {
+                    // the row's maximum, the same in its four lanes
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2));
+                    const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
+                    const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
+                    const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
+                    const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
+                    l0 *= f0;
+                    l1 *= f1;
+                    m0 = n0;
+                    m1 = n1;
+                    if (t > 0) {  // O holds the tiles before: wait for the last P.V, scale the rows
+                        ok = __all_sync(kFullMask, wait(BPV + (done + t - 1) % kSBufs, (done + t - 1) / kSBufs));
+                        if (ok) {
+                            tc_fence_after();
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t r[32];
-                    tmem_ld_16x256b<8>(tO + c0, r);
-                    tmem_wait_ld();
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t o[16];
+                                tmem_ld_16x256b_x4(tO + c, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) * f0);
+                                    o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) * f0);
+                                    o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) * f1);
+                                    o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) * f1);
+                                }
+                                tmem_st_16x256b_x4(tO + c, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                }
+                {
+                    const float b0_ = m0 == -INFINITY ? 0.f : m0, b1_ = m1 == -INFINITY ? 0.f : m1;
+                    const float2 sc2 = make_float2(sc, sc), n0 = make_float2(-b0_, -b0_), n1 = make_float2(-b1_, -b1_);
+                    float2 r0 = make_float2(0.f, 0.f), r1 = make_float2(0.f, 0.f);
+                    uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        *reinterpret_cast<uint2 *>(o + row0 * Sh::PITCH + c0 + 8 * i + 2 * ga) =
-                            make_uint2(r[4 * i], r[4 * i + 1]);
-                        *reinterpret_cast<uint2 *>(o + row1 * Sh::PITCH + c0 + 8 * i + 2 * ga) =
-                            make_uint2(r[4 * i + 2], r[4 * i + 3]);
+                        const float2 x0 = __ffma2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
+                                                     sc2, n0);
+                        const float2 x1 = __ffma2_rn(
+                            make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), sc2, n1);
+                        w[2 * i] = pack2<T>(fast_exp2(x0.x), fast_exp2(x0.y));
+                        w[2 * i + 1] = pack2<T>(fast_exp2(x1.x), fast_exp2(x1.y));
+                        add_pair<T>(r0, w[2 * i]);
+                        add_pair<T>(r1, w[2 * i + 1]);
                     }
+                    if (ok) {
+                        tmem_st_16x128b_x8(tS, w);
+                        tmem_wait_st();
+                    }
+                    l0 += r0.x + r0.y;
+                    l1 += r1.x + r1.y;
                 }
                 tc_fence_before();
+                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(bar(BPF + sb));
             }
-        } else if (ok) {
-            tc_fence_after();
-            const float inv0 = L0 > 0.f ? 1.f / L0 : 0.f, inv1 = L1 > 0.f ? 1.f / L1 : 0.f;
-            // one swap with the neighbouring lane gives each lane four consecutive columns, so
-            // that a store instruction writes whole sectors of eight rows
-            const bool odd = (ga & 1) != 0;
-            auto write = [&](auto out_tag) {
-                using OT = decltype(out_tag);
-                OT *outp = static_cast<OT *>(p.out);
-                const int gl = p.group_log2;
-                const int tok0 = it.tok + (row0 >> gl), tok1 = it.tok + (row1 >> gl);
-                const int gm = (1 << gl) - 1, h = it.g << gl;
-                const int64_t base0 = ((int64_t)(it.q0 + tok0) * p.num_heads + h + (row0 & gm)) * D;
-                const int64_t base1 = ((int64_t)(it.q0 + tok1) * p.num_heads + h + (row1 & gm)) * D;
+            // ---- output
+            ok = ok && (n == 0 || __all_sync(kFullMask, wait(BPV + (done + n - 1) % kSBufs, (done + n - 1) / kSBufs)));
+            float L0 = l0 + __shfl_xor_sync(kFullMask, l0, 1), L1 = l1 + __shfl_xor_sync(kFullMask, l1, 1);
+            L0 += __shfl_xor_sync(kFullMask, L0, 2);
+            L1 += __shfl_xor_sync(kFullMask, L1, 2);
+            if constexpr (SPLIT) {
+                // into shared memory, over Q and the rings: every product that reads them is done
+                if (ga == 0) {
+                    float *ml = reinterpret_cast<float *>(smem + Sh::OFF_M);
+                    ml[row0] = m0;
+                    ml[row1] = m1;
+                    ml[kBM + row0] = L0;
+                    ml[kBM + row1] = L1;
+                }
+                if (ok && n > 0) {
+                    tc_fence_after();
+                    float *o = reinterpret_cast<float *>(smem);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t r[32];
-                    tmem_ld_16x256b<8>(tO + c0, r);
-                    tmem_wait_ld();
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint32_t r[32];
+                        tmem_ld_16x256b<8>(tO + c0, r);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int rh = 0; rh < 2; ++rh) {
-                        const float rinv = rh ? inv1 : inv0;
-                        const int64_t base = (rh ? base1 : base0) + c0;
+                        for (int i = 0; i < 8; ++i) {
+                            *reinterpret_cast<uint2 *>(o + row0 * Sh::PITCH + c0 + 8 * i + 2 * ga) =
+                                make_uint2(r[4 * i], r[4 * i + 1]);
+                            *reinterpret_cast<uint2 *>(o + row1 * Sh::PITCH + c0 + 8 * i + 2 * ga) =
+                                make_uint2(r[4 * i + 2], r[4 * i + 3]);
+                        }
+                    }
+                    tc_fence_before();
+                }
+            } else if (ok) {
+                tc_fence_after();
+                const float inv0 = L0 > 0.f ? 1.f / L0 : 0.f, inv1 = L1 > 0.f ? 1.f / L1 : 0.f;
+                // one swap with the neighbouring lane gives each lane four consecutive columns, so
+                // that a store instruction writes whole sectors of eight rows
+                const bool odd = (ga & 1) != 0;
+                auto write = [&](auto out_tag) {
+                    using OT = decltype(out_tag);
+                    OT *outp = static_cast<OT *>(p.out);
+                    const int gl = p.group_log2;
+                    const int tok0 = cur.tok + (row0 >> gl), tok1 = cur.tok + (row1 >> gl);
+                    const int gm = (1 << gl) - 1, h = cur.g << gl;
+                    const int64_t base0 = ((int64_t)(cur.q0 + tok0) * p.num_heads + h + (row0 & gm)) * D;
+                    const int64_t base1 = ((int64_t)(cur.q0 + tok1) * p.num_heads + h + (row1 & gm)) * D;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 64) {
+                        uint32_t r[32];
+                        tmem_ld_16x256b<8>(tO + c0, r);
+                        tmem_wait_ld();
+                        if (c0 + 64 == D) {  // the next item may write O
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(BOE));
+                        }
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const int e0 = 4 * i + 2 * rh, e1 = 4 * (i + 1) + 2 * rh;
-                            const float2 near = make_float2(__uint_as_float(r[e0]) * rinv, __uint_as_float(r[e0 + 1]) * rinv);
-                            const float2 far = make_float2(__uint_as_float(r[e1]) * rinv, __uint_as_float(r[e1 + 1]) * rinv);
-                            const int col = odd ? 8 * (i + 1) + 2 * (ga - 1) : 8 * i + 2 * ga;
-                            const bool inside = (rh ? tok1 : tok0) < it.Lq;
-                            if constexpr (std::is_same<OT, float>::value) {
-                                const float2 keep = odd ? far : near, send = odd ? near : far;
-                                const float2 got = make_float2(__shfl_xor_sync(kFullMask, send.x, 1),
-                                                               __shfl_xor_sync(kFullMask, send.y, 1));
-                                const float2 a = odd ? got : keep, b = odd ? keep : got;
-                                if (inside) *reinterpret_cast<float4 *>(outp + base + col) = make_float4(a.x, a.y, b.x, b.y);
-                            } else {
-                                using PT = typename std::conditional<std::is_same<OT, __half>::value, F16, BF16>::type;
-                                const uint32_t wn = pack2<PT>(near.x, near.y), wf = pack2<PT>(far.x, far.y);
-                                const uint32_t got = __shfl_xor_sync(kFullMask, odd ? wn : wf, 1);
-                                if (inside)
-                                    *reinterpret_cast<uint2 *>(outp + base + col) =
-                                        odd ? make_uint2(got, wf) : make_uint2(wn, got);
+                        for (int rh = 0; rh < 2; ++rh) {
+                            const float rinv = rh ? inv1 : inv0;
+                            const int64_t base = (rh ? base1 : base0) + c0;
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const int e0 = 4 * i + 2 * rh, e1 = 4 * (i + 1) + 2 * rh;
+                                const float2 near = make_float2(__uint_as_float(r[e0]) * rinv, __uint_as_float(r[e0 + 1]) * rinv);
+                                const float2 far = make_float2(__uint_as_float(r[e1]) * rinv, __uint_as_float(r[e1 + 1]) * rinv);
+                                const int col = odd ? 8 * (i + 1) + 2 * (ga - 1) : 8 * i + 2 * ga;
+                                const bool inside = (rh ? tok1 : tok0) < cur.Lq;
+                                if constexpr (std::is_same<OT, float>::value) {
+                                    const float2 keep = odd ? far : near, send = odd ? near : far;
+                                    const float2 got = make_float2(__shfl_xor_sync(kFullMask, send.x, 1),
+                                                                   __shfl_xor_sync(kFullMask, send.y, 1));
+                                    const float2 a = odd ? got : keep, b = odd ? keep : got;
+                                    if (inside) *reinterpret_cast<float4 *>(outp + base + col) = make_float4(a.x, a.y, b.x, b.y);
+                                } else {
+                                    using PT = typename std::conditional<std::is_same<OT, __half>::value, F16, BF16>::type;
+                                    const uint32_t wn = pack2<PT>(near.x, near.y), wf = pack2<PT>(far.x, far.y);
+                                    const uint32_t got = __shfl_xor_sync(kFullMask, odd ? wn : wf, 1);
+                                    if (inside)
+                                        *reinterpret_cast<uint2 *>(outp + base + col) =
+                                            odd ? make_uint2(got, wf) : make_uint2(wn, got);
+                                }
                             }
                         }
                     }
-                }
-            };
-            if (p.out_dtype == PA_F32)
-                write(float{});
-            else if (p.out_dtype == PA_F16)
-                write(__half{});
-            else
-                write(__nv_bfloat16{});
-            tc_fence_before();
+                };
+                if (p.out_dtype == PA_F32)
+                    write(float{});
+                else if (p.out_dtype == PA_F16)
+                    write(__half{});
+                else
+                    write(__nv_bfloat16{});
+                tc_fence_before();
+            }
+            if constexpr (!SPLIT) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(BIE + (k & 1)));
+            }
         }
         if (!ok) *abort_v = 1;
     }

@@ -559,6 +559,66 @@ def test_many_kv_heads():
     check(prefill, make_case(BF16, 96, 24, 64, 8, [33, 200, 77], 50, 3, chunks=[33, 70, 2], seed=66), FP32, True)
 
 
+# More items than CTAs fit at once: a CTA goes on with the items of CTAs that have not started.
+
+@pytest.mark.parametrize("dtype,D,bs", [(BF16, 64, 8), (FP16, 128, 16)])
+def test_prefill_more_items_than_places(dtype, D, bs):
+    rng = np.random.default_rng(D)
+    same = make_case(dtype, 64, 8, D, bs, [int(c) for c in rng.integers(130, 500, 12)], 100, 3, chunks=[130] * 12,
+                     seed=90)
+    check(prefill, same, FP32, True)
+    lens = [int(n) for n in rng.integers(0, 300, 14)] + [0, 1, 16, 17]
+    ragged = make_case(dtype, 64, 8, D, bs, [n + int(c) for n, c in zip(lens, rng.integers(0, 300, 18))], 70, 9,
+                       chunks=lens, seed=91)
+    check(prefill, ragged, dtype, True)
+
+
+def test_prefill_more_items_than_places_with_bad_chunks_among_them():
+    # invalid sequences leave items without rows between the others
+    case = make_case(BF16, 64, 8, 64, 16, [200] * 16, 90, 2, chunks=[128] * 16, seed=92)
+    t = case.cuda()
+    good = prefill(case, t=t)
+    bad = [0, 3, 4, 5, 11, 15]
+    t["ctx"][bad] = 100                                # fewer keys than rows
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = prefill(case, t=t, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 8
+    for s in range(16):
+        rows = slice(128 * s, 128 * s + 128)
+        assert (out[rows] == 7).all() if s in bad else torch.equal(out[rows], good[rows])
+    t["ctx"][:] = 100                                  # no item has rows
+    assert (prefill(case, t=t, status=status) == 7).all()
+
+
+def test_prefill_more_items_than_places_on_streams_and_in_graphs():
+    cases = [make_case(BF16, 64, 8, 128, 16, [300] * 6, 128, 4, chunks=[200] * 6, seed=93),
+             make_case(BF16, 64, 8, 128, 16, [400, 260, 90, 300] * 2, 60, 0, chunks=[250, 260, 33, 100] * 2, seed=94)]
+    ts = [c.cuda() for c in cases]
+    want = [prefill(c, t=t) for c, t in zip(cases, ts)]
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for c, t, o, st in zip(cases, ts, outs, streams):
+            prefill(c, t=t, out=o, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            for c, t, o in zip(cases, ts, outs):
+                prefill(c, t=t, out=o)
+    for o in outs:
+        o.zero_()
+    for _ in range(10):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    for c, w in zip(cases, want):
+        assert_close(w, c, FP32, True)
+
+
 def test_host_threads_call_at_once():
     import threading
     cases = [make_case(dt, 8, 2, D, 16, [400, 90], 128, 4, chunks=[60, 7], seed=70 + i)
