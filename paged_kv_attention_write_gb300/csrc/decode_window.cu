@@ -836,6 +836,10 @@ int launch_decode_window(const DecodeArgs &a) {
     while (cluster < 16 && pairs * cluster * 2 <= fit(cluster * 2) &&
            most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
         cluster *= 2;
+    // A second wave that few pairs start takes as long as the first: two CTAs per pair halve it (312
+    // to 384 pairs of 4096 keys 136 to 141 -> 122 to 128 us; 448 pairs are equal, of 2048 keys 77 ->
+    // 82).
+    if (pairs > slots && pairs <= slots * 4 / 3 && most >= 16 * stage_keys) cluster = 2;
     // A box of a whole block where one warp's issue of the boxes bounds a CTA (about 70 clocks
     // each: 8 pairs of 4100 keys 9.0 -> 7.7 us) or where the rows past the borders that it brings
     // along are few (1024 pairs of 4112 keys in blocks of 16, 333 -> 318 us; but 256 pairs of 1028
