@@ -852,9 +852,14 @@ int launch_decode_window(const DecodeArgs &a) {
     // to one warp: contexts of 10 to 1000 keys 52.6 -> 50.8, of 10 to 2000 90.8 -> 99 us.  Boxes of
     // 16 keys where the rows are long for the warps on an SM (320 pairs of 516 keys 26.3 -> 24.6,
     // but 1024 pairs of 132 keys 16.4 -> 17.9 us).
-    const bool by_warp = a.kv_dtype != PA_F32 && pairs > slots && most <= 1152 && pairs <= INT32_MAX;
-    const int warps = by_warp ? (int)std::min<int64_t>(8, (pairs + sms - 1) / sms) : 0;  // on an SM
-    if (by_warp) p.unit = a.block_size >= 16 && most >= 128 * warps ? 2 : 1;
+    // A step of 16 keys takes a warp 0.6 us at least, so at head dimension 64 (half the bytes) a few
+    // warps per SM fall behind: 400 pairs of 260 keys 13.5 and 14.0 us (clusters), of 1004 keys 40.3
+    // and 31.4; 800 pairs 44.3 and 47.1.
+    const int per_sm = (int)std::min<int64_t>(8, (pairs + sms - 1) / sms);
+    const bool by_warp = a.kv_dtype != PA_F32 && pairs > slots && pairs <= INT32_MAX &&
+                         most <= (per_sm * a.head_dim >= 320 ? 1152 : 384);
+    const int warps = by_warp ? per_sm : 0;
+    if (by_warp) p.unit = a.block_size >= 16 && most >= a.head_dim * per_sm ? 2 : 1;
     CUtensorMap km, vm;
     for (int i = 0; i < 2; ++i) {
         CUtensorMap *m = i ? &vm : &km;
