@@ -408,7 +408,8 @@ struct Consumer32 {
                     for (int c = 0; c < NC * 2; ++c) o[h][c] = __fmul2_rn(o[h][c], make_float2(fh, fh));
                 }
             }
-            const float w = m == -INFINITY ? 0.f : fast_exp2(s - m);
+            // before the first seen key m is -inf: masked scores weigh nothing, NaN scores stay NaN
+            const float w = fast_exp2(s - (m == -INFINITY ? 0.f : m));
             l += w;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
