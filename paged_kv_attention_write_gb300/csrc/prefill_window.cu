@@ -812,7 +812,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                 acc = make_float4(acc.x * keep, acc.y * keep, acc.z * keep, acc.w * keep);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    if (mr[r] == -INFINITY) continue;  // nothing seen (or no tile: no output there)
+                    // nothing seen (or no tile: no output there); NaN scores leave a NaN sum
+                    if (lr[r] == 0.f || r0 + r >= cs) continue;
                     const float f = fast_exp2(mr[r] - M);
                     L = fmaf(lr[r], f, L);
                     acc.x = fmaf(xr[r].x, f, acc.x);

@@ -45,3 +45,16 @@ def test_decode_nan_where_a_row_looks(dtype, G, S):
     # whole queries, and keys: one, and all of the oldest half of the window
     spoil(case, [(0, 0), (1, 2 * G - 1)], [(1, 0, 70, 70), (2, 1, 300, 400), (3, 0, 0, 8)])
     check_nan(decode, case, False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
+@pytest.mark.parametrize("D,Hkv,G,ctx,chunks", [
+    (128, 1, 8, [3000, 150, 900], [20, 3, 5]),        # items split over a cluster
+    (64, 2, 2, [3000, 150, 900], [20, 3, 5]),
+    (128, 8, 8, [700, 150, 900], [300, 30, 129]),     # items of one CTA
+])
+def test_prefill_nan_where_a_row_looks(dtype, D, Hkv, G, ctx, chunks):
+    case = make_case(dtype, Hkv * G, Hkv, D, 16, ctx, 2048, 4, chunks=chunks, seed=D)
+    # two query rows, and keys that every row of their chunk sees
+    spoil(case, [(3, 0), (chunks[0], Hkv * G - 1)], [(2, Hkv - 1, 64, 700)])
+    check_nan(prefill, case, True)
