@@ -58,3 +58,65 @@ def test_prefill_nan_where_a_row_looks(dtype, D, Hkv, G, ctx, chunks):
     # two query rows, and keys that every row of their chunk sees
     spoil(case, [(3, 0), (chunks[0], Hkv * G - 1)], [(2, Hkv - 1, 64, 700)])
     check_nan(prefill, case, True)
+
+
+# One heavy key ahead of many light ones: what the light ones weigh together must reach the output.
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def heavy_key(dtype, S, Hkv, D, N, gap, first, seed):
+    """S sequences over the same N pages-in-a-row keys: the first scores `gap`, the others N(0, 1/4);
+    all queries are alike.  The first value row is N(0, 1) times `first`, the others positive, so that
+    what they add does not cancel."""
+    g = torch.Generator().manual_seed(seed)
+    u = torch.randn(D, generator=g)
+    u /= u.norm()
+    k = torch.randn((N // 16, 16, Hkv, 1), generator=g) * 0.5 * u
+    v = torch.randn((N // 16, 16, Hkv, D), generator=g).abs() + 0.5
+    k[0, 0] = gap * u
+    v[0, 0] = torch.randn((Hkv, D), generator=g) * first
+    q = (u * D ** 0.5).expand(S, Hkv, D)
+    return [x.to(dtype).contiguous().cuda() for x in (q, k, v)]
+
+
+def reference_of(q, k, v):
+    """[Hkv][D] in 64 bits: output, sum p |v|, sum p |v - output|."""
+    N, Hkv, D = k.shape[0] * 16, k.shape[2], k.shape[3]
+    k, v = (x.view(N, Hkv, D).double() for x in (k, v))
+    p = torch.softmax(torch.einsum("hd,nhd->nh", q[0].double(), k) * D ** -0.5, 0)[:, :, None]
+    out = (p * v).sum(0)
+    return out, (p * v.abs()).sum(0), (p * (v - out).abs()).sum(0)
+
+
+def heavy_bound(refs, D, gap, adds):
+    """A score q.k (all products of one sign) is off by at most D 2^-24 of itself, twice that with the
+    scaling and exp2's argument; weights off by e move the output by e sum p |v - out|.  The two
+    bf16 parts of a weight keep 2^-16 of it.  Each of a warp's `adds` sums of 16 products is rounded to
+    fp32, by half a step, 2^-24, at most and at random (keys and values are): six deviations of
+    that for the output and as much for the sum of the weights."""
+    out, mag, centred = refs
+    e = 2 * D * 2.0 ** -24 * gap
+    return e * centred + (2.0 ** -16 + 2 * 6 * adds ** 0.5 * 2.0 ** -24) * mag
+
+
+def check_heavy(dtype, kernel, gap):
+    import paged_kv_attention_write_gb300 as pa
+    # single CTAs of four warps (too many pairs for clusters), a warp per pair, a cluster
+    S, D, N, adds = {"single": (sms() // 3 + 2, 64, 65536, 1024), "warp": (sms() // 3 + 2, 128, 1024, 64),
+                     "cluster": (1, 128, 16384, 256)}[kernel]
+    q, k, v = heavy_key(dtype, S, 8, D, N, gap, 1.0, seed=int(gap))
+    tables = torch.arange(N // 16, dtype=torch.int32, device="cuda").expand(S, -1).contiguous()
+    ctx = torch.full((S,), N, dtype=torch.int32, device="cuda")
+    out = torch.empty((S, 8, D), device="cuda")
+    pa.pa_decode_window(out, q, k, v, tables, ctx, N, N, 0, D ** -0.5)
+    refs = reference_of(q, k, v)
+    assert ((out.double() - refs[0]).abs() <= heavy_bound(refs, D, gap, adds)).all()
+
+
+@pytest.mark.parametrize("kernel", ["single", "warp", "cluster"])
+@pytest.mark.parametrize("gap", [10.0, 14.0])
+@pytest.mark.parametrize("dtype", [BF16], ids=NAMES.get)
+def test_decode_light_keys_behind_a_heavy_one(dtype, gap, kernel):
+    check_heavy(dtype, kernel, gap)
