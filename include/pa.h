@@ -349,9 +349,12 @@ int pa_decode_rope(void *out, pa_dtype out_dtype, const void *query, const void 
  * context_lens[s] - 1) over the window and the sinks.  Arguments as for pa_decode; F32, F16
  * and BF16 caches.  A sequence with context length 0 gets an all-zero row; a negative
  * context, or one past max_context_len or the block table, is reported and clamped, as in
- * pa_decode.  fp32 accumulation of fp32-accurate softmax weights for every
- * cache type.  The split of a row depends on the call's sizes (num_seqs, max_context_len,
- * window, num_sinks, heads) alone, not on the other rows' contents.
+ * pa_decode.  Sums are fp32.  The softmax weights are fp32 for F32 caches; for F16 and BF16 they
+ * enter the products as two parts of the cache's type: within 2^-16 (BF16) or 2^-22 (F16) of
+ * themselves, F16 also within 2^-32 of the row's largest.  Values that a row sees must be finite
+ * (an infinite one comes out as NaN or infinity); NaN scores give NaN rows.  The split of a
+ * row depends on the call's sizes (num_seqs, max_context_len, window, num_sinks, heads) alone,
+ * not on the other rows' contents.
  */
 int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const void *key_cache,
                      const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,

@@ -22,7 +22,8 @@
 //     S = K Q^T, O^T = V^T P.  At one query token the products are far below the tensor
 //     rate (the kernel is bound by HBM), but on the CUDA cores eight heads would bound it.
 //     P enters as a rounded part plus its rounded remainder (two products), so that the
-//     weights keep 16 bits or more, and the 16 keys of a step are summed apart from O.  Summed
+//     weights keep 2^-16 of themselves (bf16) or 2^-22 (fp16, but nothing below 2^-32 of the
+//     largest), and the 16 keys of a step are summed apart from O.  Summed
 //     into O, 65536 keys behind one that weighs e^14 of a light one came out 5.5e-4 off (now
 //     7e-6); the sums cost 0.2 to 1 % (320 pairs of 260 keys, D 64, 13.5 -> 13.7 us; 1024 pairs
 //     of 1028 keys, D 128, 87.5 -> 87.8).
@@ -50,6 +51,10 @@ namespace pa {
 namespace {
 
 constexpr float kGrowLog2 = 8.f;  // the softmax reference moves when a score exceeds it by 2^8
+// Weights against the reference times 2^kLiftLog2: fp16 has no bits below 2^-24, so weights use its
+// upper range (at most 2^(7 + 8), of 2^16).  The factor is in O and in the sum alike and cancels.
+template <class T>
+constexpr float kLiftLog2 = std::is_same<T, F16>::value ? 7.f : 0.f;
 
 struct Params {
     void *out;
@@ -272,7 +277,8 @@ struct Consumer16 {
                 }
             }
         }
-        const float m0 = m[0] == -INFINITY ? 0.f : m[0], m1 = m[1] == -INFINITY ? 0.f : m[1];
+        const float m0 = (m[0] == -INFINITY ? 0.f : m[0]) - kLiftLog2<T>;
+        const float m1 = (m[1] == -INFINITY ? 0.f : m[1]) - kLiftLog2<T>;
         const float p0 = fast_exp2(s[0] - m0), p1 = fast_exp2(s[1] - m1);
         const float p2 = fast_exp2(s[2] - m0), p3 = fast_exp2(s[3] - m1);
         l[0] += p0 + p2;

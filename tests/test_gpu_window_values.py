@@ -82,23 +82,26 @@ def heavy_key(dtype, S, Hkv, D, N, gap, first, seed):
 
 
 def reference_of(q, k, v):
-    """[Hkv][D] in 64 bits: output, sum p |v|, sum p |v - output|."""
+    """[Hkv][D] in 64 bits: output, sum p |v|, sum p |v - output|, sum |v|."""
     N, Hkv, D = k.shape[0] * 16, k.shape[2], k.shape[3]
     k, v = (x.view(N, Hkv, D).double() for x in (k, v))
     p = torch.softmax(torch.einsum("hd,nhd->nh", q[0].double(), k) * D ** -0.5, 0)[:, :, None]
     out = (p * v).sum(0)
-    return out, (p * v.abs()).sum(0), (p * (v - out).abs()).sum(0)
+    return out, (p * v.abs()).sum(0), (p * (v - out).abs()).sum(0), v.abs().sum(0)
 
 
-def heavy_bound(refs, D, gap, adds):
+def heavy_bound(dtype, refs, D, gap, adds):
     """A score q.k (all products of one sign) is off by at most D 2^-24 of itself, twice that with the
     scaling and exp2's argument; weights off by e move the output by e sum p |v - out|.  The two
-    bf16 parts of a weight keep 2^-16 of it.  Each of a warp's `adds` sums of 16 products is rounded to
+    16-bit parts of a weight keep 2^-16 (bf16) or 2^-22 (fp16) of it; a fp16 part has no bits below
+    2^-25, 2^-32 of the largest weight.  Each of a warp's `adds` sums of 16 products is rounded to
     fp32, by half a step, 2^-24, at most and at random (keys and values are): six deviations of
     that for the output and as much for the sum of the weights."""
-    out, mag, centred = refs
+    out, mag, centred, total = refs
+    part = 2.0 ** -16 if dtype == BF16 else 2.0 ** -22
+    floor = 0.0 if dtype == BF16 else 2.0 ** -32
     e = 2 * D * 2.0 ** -24 * gap
-    return e * centred + (2.0 ** -16 + 2 * 6 * adds ** 0.5 * 2.0 ** -24) * mag
+    return e * centred + (part + 2 * 6 * adds ** 0.5 * 2.0 ** -24) * mag + floor * total
 
 
 def check_heavy(dtype, kernel, gap):
@@ -112,11 +115,11 @@ def check_heavy(dtype, kernel, gap):
     out = torch.empty((S, 8, D), device="cuda")
     pa.pa_decode_window(out, q, k, v, tables, ctx, N, N, 0, D ** -0.5)
     refs = reference_of(q, k, v)
-    assert ((out.double() - refs[0]).abs() <= heavy_bound(refs, D, gap, adds)).all()
+    assert ((out.double() - refs[0]).abs() <= heavy_bound(dtype, refs, D, gap, adds)).all()
 
 
 @pytest.mark.parametrize("kernel", ["single", "warp", "cluster"])
-@pytest.mark.parametrize("gap", [10.0, 14.0])
-@pytest.mark.parametrize("dtype", [BF16], ids=NAMES.get)
+@pytest.mark.parametrize("gap", [10.0, 14.0, 17.5])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
 def test_decode_light_keys_behind_a_heavy_one(dtype, gap, kernel):
     check_heavy(dtype, kernel, gap)
