@@ -368,7 +368,11 @@ int pa_decode_window(void *out, pa_dtype out_dtype, const void *query, const voi
  * position context_lens[s] - Lq_s + i.  Arguments, invalid chunks and dtypes (F16, BF16) as
  * for pa_prefill_chunk.  Values at the positions that some row of a chunk sees must be
  * finite (a key that one row sees and another does not enters the second row's sum with
- * weight zero).  How a row's keys are split depends on the call's sizes alone.
+ * weight zero); NaN scores give NaN rows.  The softmax weights are rounded to the cache's type
+ * (F16: but to no coarser than 2^-32 of the row's largest) before the products and the row
+ * sums; the products are summed by the tensor core, which cuts off what falls below the last
+ * bits of its fp32 sum (up to 2^-24 of a row's magnitude per key).  How a row's keys are split
+ * depends on the call's sizes alone.
  */
 int pa_prefill_window(void *out, pa_dtype out_dtype, const void *query,
                       const int32_t *query_start_loc, int num_tokens, int max_query_len,

@@ -13,7 +13,9 @@
 // Per key tile: S = Q K^T (tcgen05, fp32 in TMEM, two buffers), the softmax (online, log2
 // domain, the reference moves only when a score exceeds it by 2^8), P in the cache's type
 // over the S columns, O += P V.  The row sums add the rounded weights, as the product does,
-// so that a row that one key dominates loses nothing by the rounding.
+// so that a row that one key dominates loses nothing by the rounding.  The tensor core cuts off
+// what falls below the last bits of O: of 65536 keys of 2^-20 of the first one's weight, 4 % of
+// their share is lost (up to 2^-24 of a row's magnitude per key).
 //
 // Under a window items are short (a 1024-key window: nine 128-key tiles), and what costs is
 // what does not overlap: an item's first loads, its last product, its output.  So two CTAs
@@ -60,6 +62,10 @@ namespace {
 constexpr int kThreads = 12 * 32;
 constexpr int kBM = 128, kBN = 64;  // rows of an item, keys of a tile
 constexpr float kGrowLog2 = 8.f;
+// The softmax reference lies 2^kLiftLog2 below the score that set it, so that weights use fp16's upper
+// range: it has no bits below 2^-24, and a weight is at most 2^(8 + 7), of 2^16.
+template <class T>
+constexpr float kLiftLog2 = std::is_same<T, F16>::value ? 7.f : 0.f;
 constexpr int kPlanSeqs = 2047;      // sequences whose items are listed without gaps
 
 struct Params {
@@ -573,6 +579,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         ok = wait_tmem();
         const uint32_t tL = tmem + ((uint32_t)lane0 << 16), tO = tL + kTmemO;
         const float sc = p.qk_scale_log2;
+        constexpr float kGrow = kGrowLog2 + kLiftLog2<T>;
         for (int k = 0; ok && next_item(k); ++k) {
             const Item &cur = SPLIT ? it : items[k & 1];
             const int low = cur.low, high = cur.high;
@@ -613,14 +620,14 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                     c1 = fmax3(c1, __uint_as_float(s[4 * i + 6]), __uint_as_float(s[4 * i + 7]));
                 }
                 float mx0 = fmaxf(a0, c0) * sc, mx1 = fmaxf(a1, c1) * sc;
-                if (__any_sync(kFullMask, mx0 > m0 + kGrowLog2 || mx1 > m1 + kGrowLog2)) {
+                if (__any_sync(kFullMask, mx0 > m0 + kGrow || mx1 > m1 + kGrow)) {
                     // the row's maximum, the same in its four lanes
                     mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 1));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 1));
                     mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, 2));
                     mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, 2));
-                    const bool grow0 = mx0 > m0 + kGrowLog2, grow1 = mx1 > m1 + kGrowLog2;
-                    const float n0 = grow0 ? mx0 : m0, n1 = grow1 ? mx1 : m1;
+                    const bool grow0 = mx0 > m0 + kGrow, grow1 = mx1 > m1 + kGrow;
+                    const float n0 = grow0 ? mx0 - kLiftLog2<T> : m0, n1 = grow1 ? mx1 - kLiftLog2<T> : m1;
                     const float f0 = n0 == m0 ? 1.f : fast_exp2(m0 - n0);  // 0 from -inf
                     const float f1 = n1 == m1 ? 1.f : fast_exp2(m1 - n1);
                     l0 *= f0;

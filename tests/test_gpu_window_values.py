@@ -66,14 +66,14 @@ def sms():
     return torch.cuda.get_device_properties(0).multi_processor_count
 
 
-def heavy_key(dtype, S, Hkv, D, N, gap, first, seed):
-    """S sequences over the same N pages-in-a-row keys: the first scores `gap`, the others N(0, 1/4);
-    all queries are alike.  The first value row is N(0, 1) times `first`, the others positive, so that
+def heavy_key(dtype, S, Hkv, D, N, gap, first, seed, spread=0.5):
+    """S sequences over the same N pages-in-a-row keys: the first scores `gap`, the others
+    N(0, spread^2); all queries are alike.  The first value row is N(0, 1) times `first`, the others positive, so that
     what they add does not cancel."""
     g = torch.Generator().manual_seed(seed)
     u = torch.randn(D, generator=g)
     u /= u.norm()
-    k = torch.randn((N // 16, 16, Hkv, 1), generator=g) * 0.5 * u
+    k = torch.randn((N // 16, 16, Hkv, 1), generator=g) * spread * u
     v = torch.randn((N // 16, 16, Hkv, D), generator=g).abs() + 0.5
     k[0, 0] = gap * u
     v[0, 0] = torch.randn((Hkv, D), generator=g) * first
@@ -123,3 +123,25 @@ def check_heavy(dtype, kernel, gap):
 @pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
 def test_decode_light_keys_behind_a_heavy_one(dtype, gap, kernel):
     check_heavy(dtype, kernel, gap)
+
+
+def test_prefill_fp16_weights_near_the_smallest_number():
+    """Weights of 1.4 x 2^-24 of the first key's, which fp16 would round to 2^-24, over a value too
+    small to hide them; items of one CTA that holds all keys."""
+    import paged_kv_attention_write_gb300 as pa
+    D, Hkv, G, T, N = 64, 8, 8, 512, 65536
+    gap = (24 - np.log2(1.4)) * np.log(2)
+    q, k, v = heavy_key(FP16, T, Hkv, D, N, gap, 2.0 ** -6, seed=1, spread=0.0)
+    starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    tables = torch.arange(N // 16, dtype=torch.int32, device="cuda").view(1, -1)
+    ctx = torch.tensor([N], dtype=torch.int32, device="cuda")
+    out = torch.empty((T, Hkv * G, D), device="cuda")
+    pa.pa_prefill_window(out, q.repeat_interleave(G, 1), starts, T, k, v, tables, ctx, N, N, 0, D ** -0.5)
+    ref, mag, centred, total = reference_of(q, k, v)  # of the last row, which sees all keys
+    # scores as in heavy_bound; a weight is off by half a step of fp16, 2^-11 of itself or 2^-32 of
+    # the largest, in the product and in the sum alike; the sum's N / 64 additions by 2^-24 each;
+    # the tensor core cuts off up to 2^-24 of the output's magnitude with every key
+    e = ((2 * D * 2.0 ** -24 * gap + 2.0 ** -11) * centred + 2.0 ** -32 * (total + N * ref.abs()) +
+         (N / 64 + N) * 2.0 ** -24 * mag)
+    for i in range(G):
+        assert ((out[-1, i::G].double() - ref).abs() <= e).all()
