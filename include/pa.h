@@ -421,11 +421,11 @@ int pa_rope_pair_axes(int32_t *pair_axis, int rope_dim, const int32_t *sections,
  * Strides are in elements, at least the row and a multiple of 16 bytes (so the three may be
  * slices of one projection's output).  query_out and the caches overlap no other tensor of
  * the call, query_out == query apart.  num_heads = 0 (query and query_out NULL) rotates and
- * writes keys only.  Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i], the
- * angle formed exactly and reduced to [-pi, pi] in fp32 (positions below 2^24 in magnitude),
- * rotation in fp32, rounded once; elements past rope_dim and values are bit copies.  A
- * pair_axis entry outside [0, num_axes) is reported (PA_DEVERR_AXIS) and its pair not
- * rotated.
+ * writes keys only.  Pair i of token t turns by positions[pair_axis[i]][t] * freqs[i], for
+ * any position and |freqs[i]| < 4: the angle is formed as a 64-bit fraction of a turn, its sine
+ * and cosine are within 2.2e-7 (F32) or 1e-6 (F16, BF16), the rotation is in fp32, rounded
+ * once; elements past rope_dim and values are bit copies.  A pair_axis entry outside
+ * [0, num_axes) is reported (PA_DEVERR_AXIS) and its pair not rotated.
  */
 int pa_reshape_and_cache_rope_axes(void *query_out, const void *query, const void *key,
                                    const void *value, void *key_cache, void *value_cache,

@@ -12,6 +12,9 @@
 // tokens in bf16 (50 MB) 10.1 us, 8 tokens 2.0 us.  CTAs of several tokens
 // (their constants loaded once) took 122, 11.1 and 2.2 us in one wave, 121 and 12.9 us with four
 // tokens each: the hardware's scheduling of many short CTAs hides the round trips better.
+#include <cmath>
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace pa {
@@ -103,21 +106,53 @@ __device__ __forceinline__ void rotate_adjacent(T t, uint4 &a, const float2 *cs,
     }
 }
 
+// The angle pos * f in turns.  Only its fraction matters, so it is formed as a 64-bit fraction, where
+// whole turns fall off by themselves (Payne and Hanek's reduction, with one word of 1 / 2 pi):
+// |f| / 2 pi to 2^-64, times pos.  (Subtracting a multiple of 2 pi in fp32 picks the wrong turn now
+// and then from positions of 2^21 on.)
+__device__ __forceinline__ uint64_t turns_per_position(float f) {
+    constexpr uint64_t kPerTurn = 0xa2f9836e4e44152aull;  // 2^66 / 2 pi
+    const uint32_t bits = __float_as_uint(f), exponent = bits >> 23 & 255u;
+    const uint64_t m = (bits & 0x7fffffu) | (exponent ? 0x800000u : 0u);  // |f| = m 2^(exponent - 150)
+    const int shift = 152 - (int)max(exponent, 1u);                       // |f| / 2 pi = m kPerTurn 2^-(64 + shift)
+    const uint64_t lo = m * kPerTurn, hi = __umul64hi(m, kPerTurn);
+    return shift <= 0 ? lo << min(-shift, 63) : shift < 64 ? hi << (64 - shift) | lo >> shift : hi >> min(shift - 64, 63);
+}
+// Its cosine and sine.  For every 32-bit position and frequencies below 4 the fraction, rounded to 32
+// bits, is off by 1.9e-9 (as an angle) at most.  fp32 caches: rounding it to fp32 adds pi 2^-25,
+// sincospif two units of the last place, 2.2e-7 in all.  16-bit caches round by 2^-11 at least, and
+// there the hardware's sine and cosine (2^-21.2) of the fraction times pi do: under 1e-6 in all, and
+// 2048 tokens take 10.1 us instead of 10.3.
+template <class T>
+__device__ __forceinline__ float2 cos_sin(int pos, uint64_t step, float f) {
+    const uint64_t turn = step * (uint64_t)(int64_t)pos;
+    const float x = (float)(int)((turn + 0x80000000ull) >> 32) * 0x1p-31f;  // in half turns, [-1, 1]
+    float s, c;
+    if constexpr (std::is_same<T, F32>::value)
+        sincospif(x, &s, &c);
+    else
+        __sincosf(x * 3.14159265358979f, &s, &c);
+    if (!(fabsf(f) < INFINITY)) c = s = NAN;
+    return make_float2(c, f < 0.f ? -s : s);
+}
+
 // (cos, sin) of token t's pairs into cs, by all threads (a row has at most kMaxPairs pairs,
 // one per thread).  The axis and frequency of a thread's pair and the token's positions on
 // every axis are read together: one round trip, where following pair -> axis -> position
 // would take two.
+template <class T>
 __device__ __forceinline__ void angles(const RopeAxesArgs &p, int t, float2 *cs) {
     __shared__ int32_t pos[PA_ROPE_MAX_AXES];
     const int i = threadIdx.x, half = p.rope.rope_dim / 2;
     const int axis = i < half ? p.rope.pair_axis[i] : 0;
     const float freq = i < half ? p.rope.freqs[i] : 0.f;
     if (i < p.rope.num_axes) pos[i] = p.positions[(int64_t)i * p.num_tokens + t];
+    const uint64_t step = turns_per_position(freq);
     __syncthreads();
     if (i < half) {
         const bool ok = axis >= 0 && axis < p.rope.num_axes;
         if (!ok && t == 0) report(p.status, PA_DEVERR_AXIS);
-        cs[i] = ok ? rope_cos_sin(pos[axis], freq) : make_float2(1.f, 0.f);  // not rotated
+        cs[i] = ok ? cos_sin<T>(pos[axis], step, freq) : make_float2(1.f, 0.f);  // not rotated
     }
     __syncthreads();
 }
@@ -179,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rope_axes_kernel(const RopeA
         }
     };
     load(h0);
-    angles(p, t, cs);
+    angles<T>(p, t, cs);
     const bool write = slot >= 0 && slot < (int64_t)p.num_blocks * p.block_size;
     if (slot >= 0 && !write && threadIdx.x == 0) report(p.status, PA_DEVERR_SLOT);
     const int todo = write ? heads : Hq;
@@ -249,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) rope_axes_odd_halves_kernel(const Ro
     pdl_wait_previous();
     pdl_launch_dependents();
     const int t = blockIdx.x, D = p.head_dim, half = p.rope.rope_dim / 2;
-    angles(p, t, cs);
+    angles<T>(p, t, cs);
     rotate_elements(static_cast<ST *>(p.query_out) + (int64_t)t * p.num_heads * D,
                     static_cast<const ST *>(p.query) + t * p.query_stride, cs, p.num_heads, D, half);
     const int64_t slot = p.slot_mapping[t];
