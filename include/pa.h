@@ -275,9 +275,10 @@ int pa_copy_blocks(void *key_cache, void *value_cache, const int64_t *block_mapp
  *
  * Pair i (i < rope_dim / 2) of a row at position pos is rotated by the angle
  * pos * freqs[i]:  (x, y) -> (x cos - y sin, x sin + y cos).  The angle is formed exactly
- * (as a sum of two floats) and reduced to [-pi, pi] in fp32 (within 2.3e-7 of the exact
- * reduced angle for |pos| < 2^24; positions beyond lose that bound), its sine and cosine
- * taken in fp32 (absolute error below 4e-7), the rotation done in fp32.  Elements past
+ * (as a sum of two floats) and reduced by whole turns in fp32 (within 2.4e-7 of the exact
+ * angle less those turns for |pos| < 2^24; positions beyond lose that bound), its sine and cosine
+ * taken in fp32 (in all within 6e-7 for |pos| < 2^17 and freqs up to 1, 9e-7 for |pos| < 2^24,
+ * as measured), the rotation done in fp32.  Elements past
  * rope_dim are not rotated.  The 1/sqrt(head_dim) factor stays the attention's `scale`
  * argument.
  */
