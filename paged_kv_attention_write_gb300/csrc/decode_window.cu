@@ -598,10 +598,12 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             if (lane == 0) mbar_arrive(empty0 + 8 * st);
         }
         // ---- the warps' results into the ring (every box of it has landed and been read)
+        __syncwarp();  // the barriers are of the aligned form
         named_barrier(1, NW * 32);
         float *red_m = reinterpret_cast<float *>(smem) + NW * HW * Sh::PITCH, *red_l = red_m + NW * HW;
         float *red_o = reinterpret_cast<float *>(smem);
         work.finish(red_o + warp * HW * Sh::PITCH, red_m + warp * HW, red_l + warp * HW);
+        __syncwarp();
         named_barrier(1, NW * 32);
         // ---- joined over the warps: head h is row h % HW of the warps w with w % QS == h / HW
         const int heads = G ? G : p.group;
@@ -635,7 +637,6 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
     }
     if (CS == 1) return;
     // ---- joined over the cluster: each CTA writes its share of the row
-    __syncwarp();
     cluster_sync();
     const int heads = G ? G : p.group;
     const int total = heads * (D / 2), i0 = total * rank / CS, i1 = total * (rank + 1) / CS;

@@ -786,7 +786,6 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
     if (SPLIT && live) {
         // ---- the CTAs' outputs joined: each writes its share of the rows
-        __syncwarp();
         cluster_sync();
         const int cs = (int)cluster_size(), rows = kBM / cs, first = (int)cluster_rank() * rows;
         const uint32_t a_o = sQ, a_m = sQ + Sh::OFF_M, a_l = sQ + Sh::OFF_L;

@@ -1,10 +1,11 @@
-"""Values that a windowed call meets beside ordinary numbers: NaN where a row looks."""
+"""Windowed calls beside ordinary numbers and sizes: NaN where a row looks, weights of all magnitudes,
+shares of a row smaller than a warp."""
 import numpy as np
 import pytest
 import torch
 
 from test_gpu_window import BF16, FP16, FP32, NAMES, decode, prefill
-from window_cases import bound, make_case, reference
+from window_cases import assert_close, bound, make_case, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +146,25 @@ def test_prefill_fp16_weights_near_the_smallest_number():
          (N / 64 + N) * 2.0 ** -24 * mag)
     for i in range(G):
         assert ((out[-1, i::G].double() - ref).abs() <= e).all()
+
+
+# Shares of a row that part a warp's lanes before the cluster's last barrier.
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("Hkv,G,D", [(1, 1, 64), (1, 1, 128), (2, 1, 64), (4, 1, 64), (1, 2, 64), (8, 1, 128)])
+def test_decode_shares_smaller_than_a_warp(dtype, Hkv, G, D):
+    # one row of G x D / 2 pairs over up to sixteen CTAs: 2 to 64 per CTA
+    case = make_case(dtype, Hkv * G, Hkv, D, 16, [5000], 4096, 4, seed=D + G)
+    for _ in range(20):
+        out = decode(case, FP32)
+    assert_close(out, case, FP32, False)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 5, 17, 31])
+@pytest.mark.parametrize("Hkv,G,D", [(1, 1, 64), (2, 1, 128), (1, 2, 64)])
+def test_prefill_shares_that_end_inside_a_warp(rows, Hkv, G, D):
+    # chunks whose rows end within a CTA's share: some lanes leave the last loop early
+    case = make_case(BF16, Hkv * G, Hkv, D, 16, [3000], 2048, 4, chunks=[rows], seed=rows)
+    for _ in range(20):
+        out = prefill(case, FP32)
+    assert_close(out, case, FP32, True)
