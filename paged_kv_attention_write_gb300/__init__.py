@@ -430,8 +430,9 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
     if value.dtype is not dt or key_cache.dtype is not dt or value_cache.dtype is not dt:
         _refuse(what, "query, keys, values and caches share one dtype")
     if slot_mapping.dtype is not torch.int64 or slot_mapping.shape != (T,) or positions.dtype is not torch.int32 or (
-            positions.shape != (rope.num_axes, T)) or (status is not None and status.dtype is not torch.int32):
-        _refuse(what, "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32")
+            positions.shape != (rope.num_axes, T)) or (
+            status is not None and (status.dtype is not torch.int32 or status.numel() < 1)):
+        _refuse(what, "slot_mapping is int64 [T], positions int32 [num_axes][T], status int32 [1]")
     if not (key_cache.is_contiguous() and value_cache.is_contiguous() and slot_mapping.is_contiguous() and
             positions.is_contiguous()):
         _refuse(what, "caches, query_out, slots and positions must be contiguous")

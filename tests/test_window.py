@@ -265,6 +265,16 @@ def test_rope_axes_python_refusals(pa, over, why):
     assert e.value.code == -1
 
 
+@pytest.mark.parametrize("status", [torch.zeros(0, dtype=torch.int32), torch.zeros(1, dtype=torch.int64)])
+def test_status_words_that_hold_nothing_are_refused(pa, status):
+    q, k = torch.zeros(5, 4, 64, dtype=torch.bfloat16), torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(3, 8, 2, 64, dtype=torch.bfloat16)
+    rope = pa.RopeAxes(torch.zeros(32), torch.zeros(32, dtype=torch.int32), 64, 3)
+    with pytest.raises(pa.PAError, match="status"):
+        pa.pa_reshape_and_cache_rope_axes(q.clone(), q, k, k, pool, pool, torch.zeros(5, dtype=torch.int64),
+                                          torch.zeros(3, 5, dtype=torch.int32), rope, status=status)
+
+
 def test_rope_axes_argument_record_refusals(pa):
     f, a = torch.zeros(32), torch.zeros(32, dtype=torch.int32)
     for bad in ((f.double(), a, 64, 3), (f, a.long(), 64, 3), (f[:16], a, 64, 3), (f, a, 62, 3), (f[::2], a[::2], 32, 3)):
