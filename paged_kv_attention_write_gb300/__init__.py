@@ -81,7 +81,7 @@ _lib.pa_decode_rope.argtypes = [_vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, 
 def _send(name: str, f, record: struct.Struct, *fields) -> None:
     try:
         args = record.pack(*fields)
-    except (struct.error, OverflowError) as e:  # not an integer, or one past 32 bits; a scale past fp32
+    except struct.error as e:  # not an integer, or one past 32 bits
         raise PAError(-1, f"{name}: {e}") from None
     rc = f(args)
     if rc != 0:
