@@ -40,7 +40,8 @@
 // fp32 caches, 64 sequences x 2052 keys, 8 kv heads, D 128: 155 (1 query head per kv head, 6.9
 // TB/s), 159 (4), 183 (8).  CTAs of eight consumer warps, one per SM, took 164, 171 and 210:
 // nothing ran under their beginnings and ends.
-// Every mbarrier wait is bounded in time.
+// Every mbarrier wait is bounded in time; if one gives up, the boxes under way still land before the
+// CTA leaves (not run on a GPU: it would take a wait of two seconds).
 #include <algorithm>
 #include <type_traits>
 
@@ -548,8 +549,8 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
         auto block_id = [&](int i) {
             return mine && v0 + i * NGRP + slot < v1 ? bt[group_of(i) / per_block] : -1;
         };
-        int next = block_id(0);
-        for (int i = 0; i < stages; ++i) {
+        int next = block_id(0), i = 0;
+        for (; i < stages; ++i) {
             const int id = next;
             next = block_id(i + 1);
             const int st = i % NSTAGE;
@@ -580,6 +581,10 @@ decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_cons
             }
             __syncwarp();
         }
+        // every box has landed before the warp leaves, whether or not a wait gave up
+        bool landed = true;
+        for (int j = max(0, i - NSTAGE); j < i && landed; ++j)
+            landed = mbar_wait(full0 + 8 * (j % NSTAGE), (j / NSTAGE) & 1, p.status);
     } else {
         // ============================================================ consumers
         typename std::conditional<Sh::kF32, Consumer32<D, G ? G : 1>, Consumer16<T, D>>::type work(p, warp, lane, s, g);
@@ -743,8 +748,14 @@ decode_window_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid
         loaded = (loaded & ~(3u << 2 * slot)) | (unit == 1 ? boxes & 3u : boxes & 1u ? 3u : 0u) << 2 * slot;
     };
     for (int t = 0; t < depth && t < steps; ++t) issue(t, t);
-    int slot = 0, phase = 0;
-    for (int t = 0; t < steps; ++t) {
+    int slot = 0, phase = 0, t = 0;
+    auto advance = [&] {
+        if (++slot == depth) {
+            slot = 0;
+            phase ^= 1;
+        }
+    };
+    for (; t < steps; ++t, advance()) {
         if (!__all_sync(kFullMask, mbar_wait(full0 + 8 * slot, phase, p.status))) break;
         const uint32_t kb = ring + slot * STEP, valid = loaded >> 2 * slot & 3u;
         const bool wrote = valid && work.pair(p, keys, kb, kb + 2 * GB, 2 * t, valid);
@@ -754,11 +765,10 @@ decode_window_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid
             __syncwarp();
             issue(t + depth, slot);
         }
-        if (++slot == depth) {
-            slot = 0;
-            phase ^= 1;
-        }
     }
+    // if a wait gave up: the boxes under way land before the CTA leaves
+    for (const int end = min(t + depth, steps); t < end; ++t, advance())
+        if (!__all_sync(kFullMask, mbar_wait(full0 + 8 * slot, phase, p.status))) break;
     // the heads' rows through shared memory, so that the stores are contiguous
     __syncwarp();
     float *red_o = reinterpret_cast<float *>(smem), *red_m = red_o + Sh::HW * Sh::PITCH, *red_l = red_m + Sh::HW;
