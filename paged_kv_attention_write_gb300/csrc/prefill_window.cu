@@ -49,7 +49,8 @@
 // Warps: 0 items, TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the
 // rows of V that no row of the item looks at, so that stale or NaN slots never meet a zero
 // weight), 4-11 softmax and output, each a 16-row slab through the 16-lane TMEM shapes.
-// Every mbarrier wait is bounded in time.
+// Every mbarrier wait is bounded in time; if one gives up, loads and products under way still end before
+// the CTA frees its TMEM and leaves (not run on a GPU: it would take a wait of two seconds).
 #include <algorithm>
 #include <type_traits>
 
@@ -283,7 +284,8 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     constexpr int BIF = BOE + 1;      // item slot written
     constexpr int BIE = BIF + 2;      // item slot read by warps 1-11
     constexpr int BCL = BIE + 2;      // answer to the request for another item
-    constexpr int NBAR = BCL + 1;
+    constexpr int BDR = BCL + 1;      // products of warps 1 and 3 finished (only after a wait gave up)
+    constexpr int NBAR = BDR + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + NBAR);
     int *abort_flag = reinterpret_cast<int *>(bars + NBAR) + 1;
     constexpr int OFF_ANSWER = 352, OFF_ITEMS = 368;
@@ -422,7 +424,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             }
             ++asked;
         };
-        for (int k = 0; ok; ++k) {
+        int k = 0, t = 0;  // queries and (beside `done`) key tiles whose loads have been issued
+        for (; ok; ++k) {
+            if (SPLIT && k > 0) break;
+            t = 0;
             if (SPLIT || !is_k) {
                 if (!next_item(k)) break;
             } else {
@@ -470,9 +475,10 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                     }
                 }
                 ok = __shfl_sync(kFullMask, w_ok, 0);
+                if (!ok) break;
             }
 #pragma unroll 1
-            for (int t = 0; ok && t < n; ++t) {
+            for (; t < n; ++t) {
                 const int id = id0;
                 id0 = id1;
                 id1 = block_id(t + 2);
@@ -487,13 +493,18 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                     if (w_ok) mbar_arrive_expect_tx(bar(full + st), bytes);
                 }
                 ok = __shfl_sync(kFullMask, w_ok, 0);
-                if (ok && valid)
+                if (!ok) break;
+                if (valid)
                     tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
                                 bar(full + st), policy);
                 __syncwarp();
                 if (!SPLIT && is_k && t == n - 1) ask();
             }
         }
+        // the last loads land before the warp leaves, also when a wait gave up
+        bool landed = !is_k || k == 0 || mbar_wait(bar(BQF), (k - 1) & 1, p.status);
+        for (int j = max(0, done + t - NS); j < done + t && landed; ++j)
+            landed = mbar_wait(bar(full + j % NS), (j / NS) & 1, p.status);
         if (!SPLIT && asked > heard) mbar_wait(bar(BCL), heard & 1, p.status);  // no answer is left to land
         if (!ok) *abort_v = 1;
     } else if (warp == 1) {
@@ -847,6 +858,13 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (live && *abort_v) {  // a wait gave up: the products under way end before TMEM and shared memory go
+        if (lane == 0 && (warp == 1 || warp == 3)) {
+            mma_commit(bar(BDR + warp / 2));
+            mbar_wait(bar(BDR + warp / 2), 0, p.status);
+        }
+        __syncthreads();
+    }
     if (live && warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
