@@ -168,3 +168,38 @@ def test_prefill_shares_that_end_inside_a_warp(rows, Hkv, G, D):
     for _ in range(20):
         out = prefill(case, FP32)
     assert_close(out, case, FP32, True)
+
+
+# Single CTAs, most of them taking whole blocks (from 64 blocks' keys on): more pairs than a second wave of two CTAs each would start
+# (4 / 3 of two per SM), rows past 1152 keys where the cache is of 16 bits (shorter ones take a
+# warp per pair).  Between one wave and that, a pair takes two CTAs.
+
+def many_pairs(dtype, D, bs, G, window, sinks, pairs_per_two_sms, seed):
+    Hkv = 8
+    S = int(sms() * 2 * pairs_per_two_sms) // Hkv + 1
+    rng = np.random.default_rng(seed)
+    ctx = [0, 1, window, window + sinks, window + bs - 1] + [int(c) for c in rng.integers(0, window + 300, S - 5)]
+    return make_case(dtype, Hkv * G, Hkv, D, bs, ctx, window, sinks, seed=seed)
+
+
+@pytest.mark.parametrize("dtype,D,bs,G,window,sinks", [
+    (FP32, 64, 16, 1, 1023, 9), (FP32, 64, 32, 8, 2050, 4), (FP32, 128, 16, 4, 1020, 20), (FP32, 128, 32, 2, 777, 0),
+    (BF16, 128, 16, 8, 1200, 20), (BF16, 128, 32, 1, 1300, 3), (FP16, 128, 16, 1, 1250, 16), (FP16, 128, 32, 8, 1153, 5),
+    (BF16, 64, 32, 8, 1200, 33), (FP16, 64, 16, 4, 1300, 0), (BF16, 128, 8, 4, 1199, 7)])
+def test_decode_single_ctas_of_several_stages(dtype, D, bs, G, window, sinks):
+    case = many_pairs(dtype, D, bs, G, window, sinks, 1.45, seed=bs + G)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert_close(decode(case, FP32, status), case, FP32, False)
+    assert status.item() == 0
+
+
+def test_decode_wide_windows_of_a_full_server():
+    # eight query heads per kv head behind 4096 keys and 16 sinks, in blocks of 16
+    case = many_pairs(FP16, 128, 16, 8, 4096, 16, 1.45, seed=7)
+    assert_close(decode(case, FP16), case, FP16, False)
+
+
+@pytest.mark.parametrize("dtype,D", [(FP32, 64), (FP32, 128), (BF16, 128), (FP16, 64)])
+def test_decode_two_ctas_per_pair(dtype, D):
+    case = many_pairs(dtype, D, 16, 2, 2100, 9, 1.15, seed=D)
+    assert_close(decode(case, FP32), case, FP32, False)
