@@ -64,7 +64,9 @@ int pa_engine_attend(const pa_engine_cache *cache, const pa_sched_batch *batch,
 /*
  * pa_engine_attend_window -- pa_engine_attend under a sliding window with sinks: the same
  * block copies and cache write (pa_reshape_and_cache), then pa_decode_window or
- * pa_prefill_window with `window` and `num_sinks` (their rules; no workspace).
+ * pa_prefill_window with `window` and `num_sinks` (their rules; no workspace).  It frees
+ * nothing: the scheduler holds a sequence's blocks, those behind the window too, until the
+ * sequence ends.
  */
 int pa_engine_attend_window(const pa_engine_cache *cache, int window, int num_sinks,
                             const pa_sched_batch *batch, const pa_sched_offsets *offsets,

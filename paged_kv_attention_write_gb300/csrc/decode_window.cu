@@ -33,8 +33,8 @@
 // take one warp, a CTA of its own, per pair instead: it issues its own boxes into its own ring
 // and joins nothing.  In the clusters' kernel such pairs wait for the start and the end of a
 // CTA of five warps, two of them at a time on an SM; here up to eight pairs are in flight.
-// Measured (bf16 or fp16, D 128, GPU us): 128 sequences x 4112 keys, 64 q / 8 kv heads 313
-// (6.85 TB/s, the measured copy rate is 6.68); 32 x 1028, 32 / 8 heads 23.0 (5.7 TB/s: 256 CTAs
+// Measured (bf16 or fp16, D 128, GPU us): 128 sequences x 4112 keys, 64 q / 8 kv heads 314
+// (6.83 TB/s, the measured copy rate is 6.68); 32 x 1028, 32 / 8 heads 23.1 (5.7 TB/s: 256 CTAs
 // of 17 stages, the first loads and the last merges show); 1 x 516 5.5, 1 x 4100 7.7 (launch,
 // a chain of context -> block table -> box -> scores -> joins).
 // fp32 caches, 64 sequences x 2052 keys, 8 kv heads, D 128: 155 (1 query head per kv head, 6.9
@@ -489,7 +489,7 @@ struct Consumer32 {
 };
 
 // grid = (cluster size, kv heads, sequences), cluster (cluster size, 1, 1).  G is the group
-// size for fp32 caches; 0 (any group up to 8) for 16-bit ones.
+// size for fp32 caches; 0 (groups of 1, 2, 4 or 8) for 16-bit ones.
 template <class T, int D, int G>
 __global__ void __launch_bounds__(Shape<T, D>::THREADS, 2)
 decode_window_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,

@@ -10,16 +10,16 @@
 // row, packed into one list of virtual blocks (a few sinks cost one block, not a key tile)
 // and cut into tiles of 64 virtual keys.  Only tiles at a border are masked.
 //
-// Per key tile: S = Q K^T (tcgen05, fp32 in TMEM, two buffers), the softmax (online, log2
-// domain, the reference moves only when a score exceeds it by 2^8), P in the cache's type
-// over the S columns, O += P V.  The row sums add the rounded weights, as the product does,
+// Per key tile: S = Q K^T (tcgen05, fp32 in TMEM; kSBufs buffers: two at head dimension 128, three
+// at 64), the softmax (online, log2 domain, the reference moves only when a score exceeds it by
+// 2^8), P in the cache's type over the S columns, O += P V.  The row sums add the rounded weights, as the product does,
 // so that a row that one key dominates loses nothing by the rounding.  The tensor core cuts off
 // what falls below the last bits of O: of 65536 keys of 2^-20 of the first one's weight, 4 % of
 // their share is lost (up to 2^-24 of a row's magnitude per key).
 //
 // Under a window items are short (a 1024-key window: nine 128-key tiles), and what costs is
 // what does not overlap: an item's first loads, its last product, its output.  So two CTAs
-// share an SM, each with half of TMEM (two 64-column S buffers and O) and of the shared
+// share an SM, each with half of TMEM (the 64-column S buffers and O) and of the shared
 // memory, and one's tiles run under the other's beginning and end; every scheduler has four
 // softmax warps.  The grid is one CTA per item, but a CTA whose loads near their end calls off
 // one that has not started (cluster launch control) and goes on with its item: Q, keys and the
@@ -31,7 +31,7 @@
 //
 // Measured (us; 8 chunks of 512 tokens, 64 q / 8 kv heads, window 4096, fp16 | 4 chunks of
 // 512, 32 / 8, window 1024, bf16 | 9 ragged chunks, 16 / 16, D 64, window 301 | 16 fresh prompts
-// of 100 to 1500, 32 / 8, window 1024): this 455 | 34.9 | 23.2 | 153 (1213, 625, 168 TFLOP/s);
+// of 100 to 1500, 32 / 8, window 1024): this 459 | 34.6 | 23.3 | 150 (1202, 630, 166 TFLOP/s);
 // one item per CTA 460 | 37.6 | 23.3 | 188.  The loads of K and of V are one loop: as two copies
 // the warps' loops together miss the instruction cache (476 | 38.0).  Steps tried on the way,
 // each in its own build: CTAs that own every n-th item 507 | 45 | 28 (uneven, 9 to 68 key tiles
@@ -39,8 +39,10 @@
 // 47 | 42; two CTAs with 128-key tiles and one S buffer each 555 | 57 | 40, with S issued for two
 // 64-key tiles at once 574 | 53 | 30; two row tiles per CTA taking turns, eight softmax warps
 // each, 582 | 67 | 53.
-// What bounds it: a tile takes its CTA about 1550 clocks, nearly all of them in the softmax
-// warps (TMEM load, maxima, exponentials, P store, hand-over); the tensor core is busy 52 % of
+// What bounds it: a tile takes its CTA 0.88 us behind windows up to 1024 keys and 0.97 (bf16) to
+// 1.01 us (fp16) from 4096 on, where power holds the clocks down (1500 to 1700 clocks), nearly all
+// in the softmax warps (TMEM load, maxima, exponentials, P store, hand-over), and an item about one
+// tile more; the tensor core is busy 52 % of
 // the time and its queue 76 % (an S product of 64 keys occupies it for 48 clocks, not 32: it
 // reads 16 columns of all of Q, 4 KB, for 2 KB of K).  With no exponentials, no maxima and no P
 // stores (a timing-only build of the 507 us step) 469 us were left; with no K and V loads at
@@ -509,7 +511,7 @@ prefill_window_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (!ok) *abort_v = 1;
     } else if (warp == 1) {
         // ============================================ S_t = Q K_t^T
-        // S_t overwrites the P of tile t - 2: it waits until that P.V has finished.
+        // S_t overwrites the P of tile t - kSBufs: it waits until that P.V has finished.
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
                      : "memory");

@@ -9,7 +9,7 @@
 // the head in registers and applies them to the same place of every head it owns.
 //
 // Measured: 16384 tokens in fp32 (32 q / 8 kv heads, D 128, 805 MB) 117 us, 2048
-// tokens in bf16 (50 MB) 10.1 us, 8 tokens 2.0 us.  CTAs of several tokens
+// tokens in bf16 (50 MB) 10.2 us, 8 tokens 2.0 us.  CTAs of several tokens
 // (their constants loaded once) took 122, 11.1 and 2.2 us in one wave, 121 and 12.9 us with four
 // tokens each: the hardware's scheduling of many short CTAs hides the round trips better.
 #include <cmath>
@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rope_axes_kernel(const RopeA
 }
 
 // The halves pairing of a width whose half is not a whole number of 16-byte vectors: element
-// by element, one CTA per token.
+// by element, one CTA per token.  A rare shape, twice the time of the kernel above: 2048 tokens
+// of 32 q / 8 kv heads in bf16 22.5 us, 16384 133 (there 10.2 and 61.5).
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

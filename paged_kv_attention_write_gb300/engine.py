@@ -56,7 +56,8 @@ class PagedAttentionEngine:
                  token_budget: int = 4096, chunk_tokens: int = 512, max_decode_steps: int = 8,
                  prefix_cache: bool = True, scale: Optional[float] = None, window: Optional[int] = None,
                  num_sinks: int = 0):
-        """``window``: attend the newest ``window`` keys and the first ``num_sinks`` only."""
+        """``window``: attend the newest ``window`` keys and the first ``num_sinks`` only (the blocks
+        behind the window stay with their sequence until it ends)."""
         if (window is not None and not 1 <= window < 2 ** 31) or not 0 <= num_sinks < 2 ** 31 or (
                 num_sinks and window is None):  # 32 bits: ctypes would cut off what is above
             raise ValueError("window is at least 1, num_sinks at least 0 and only with a window")
