@@ -85,7 +85,9 @@ enum {
     PA_DEVERR_QUERY = 8,     /* query_start_loc not monotone, or a chunk longer than its context */
     PA_DEVERR_TIMEOUT = 16,  /* a bounded wait inside a kernel gave up (internal error; the
                                 kernel returned instead of hanging) */
-    PA_DEVERR_AXIS = 32      /* pa_rope_axes.pair_axis entry outside [0, num_axes) */
+    PA_DEVERR_AXIS = 32,     /* pa_rope_axes.pair_axis entry outside [0, num_axes) */
+    PA_DEVERR_FREE_LIST = 64 /* pa_tables_*: the free list ran out, its count lies outside it, or a
+                                returned block does not fit it */
 };
 
 /*
@@ -472,6 +474,128 @@ typedef struct {
 int pa_decode_window_args(const pa_window_args *args);
 int pa_prefill_window_args(const pa_window_args *args);
 int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *args);
+
+/*
+ * pa_cross_attention -- attention of packed query rows over a sequence's whole context: the
+ * states of an encoder, the patches of images, a retrieved document, written to cache slots
+ * once (pa_reshape_and_cache) and read by every later row.  Nothing is causal: row r sees the
+ * keys [begin_r, end_r) of its sequence's context.
+ *
+ *   out              [num_tokens][num_heads][head_dim], out_dtype (written)
+ *   query            [num_tokens][num_heads][head_dim], kv_dtype
+ *   query_start_loc  int32 [num_seqs + 1], non-decreasing: the rows of sequence s are
+ *                    query_start_loc[s] .. query_start_loc[s+1]-1 (one token, a beam's rows, a
+ *                    chunk).  NULL: one row each, row s of sequence s, num_tokens == num_seqs
+ *                    (max_query_len is not read)
+ *   max_query_len    >= every sequence's rows (host bound); a sequence with more is reported
+ *                    (PA_DEVERR_QUERY) and its rows left as they were
+ *   key_ranges       int32 [num_tokens][2], 8-byte aligned: (begin, end) of each row, cut to
+ *                    [0, context); NULL: every row sees its whole context
+ *   context_lens     int32 [num_seqs]: cached keys of the sequence, 0 allowed
+ *   other arguments  as for pa_decode
+ *
+ *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k_j) v_j over begin_r <= j < end_r;
+ *   a row that sees no key is all zeros.  Rows of no sequence are left as they were.
+ * F32, F16 and BF16 caches, any number of rows.  scale <= 0 returns PA_ERR_INVALID_ARG.  There
+ * is no workspace; a call may be captured into a CUDA graph after one eager call with its types
+ * and head dimension on the device.  Contexts below zero, past max_context_len or past the
+ * block table are reported and clamped.  A block-table entry is read only if a row's range
+ * reaches its block; what the cache holds in slots that no row of the sequence sees is never used,
+ * not even NaN.  Values that some row of a sequence sees must be finite (a key that one row
+ * sees and another does not may enter the second row's sum with weight zero); NaN scores give
+ * NaN rows.
+ */
+int pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, const int32_t *query_start_loc,
+                       int num_tokens, int max_query_len, const int32_t *key_ranges, const void *key_cache,
+                       const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                       const int32_t *context_lens, int max_context_len, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                       pa_dtype kv_dtype, int32_t *status, pa_stream_t stream);
+
+/*
+ * Block tables kept on the device: a step's tables, row starts, positions and slots made from
+ * the sequences' lengths, so that a step loop (captured into a CUDA graph, say) grows its own
+ * sequences and sends nothing from the host.  The free blocks are a stack in device memory:
+ * free_blocks int32 [free_capacity], of which the first *num_free are free.  These pools share no
+ * blocks between sequences (pa_kv_manager.h does, on the host).  One launch each; results do not depend on timing.
+ *
+ * pa_tables_extend -- sequence s grows from cached_lens[s] to cached_lens[s] + new_lens[s] tokens.
+ *
+ *   block_tables     int32 [num_seqs][max_blocks_per_seq]: the first ceil(cached / block_size)
+ *                    entries of a row are its blocks (read); those of the blocks it gains are
+ *                    written, the rest is left as it was
+ *   context_lens     int32 [num_seqs] (written): the new lengths; may be cached_lens itself
+ *   query_start_loc  int32 [num_seqs + 1] or NULL (written): prefix sums of new_lens, cut to
+ *                    num_tokens
+ *   positions        int32 [num_tokens] or NULL (written): position of each new token
+ *   slot_mapping     int64 [num_tokens] (written): its cache slot.  Rows behind the last sequence
+ *                    get position 0 and slot -1 (padding, which the cache writes skip)
+ *   num_free_out     int32 [1] (written): free blocks left; may be num_free itself
+ *   cached_lens,
+ *   new_lens         int32 [num_seqs]; new_lens[s] = 0 leaves the sequence as it is
+ *   free_blocks,
+ *   num_free         the stack (read): block i taken by the call, in the order of the sequences
+ *                    and of their tables, is free_blocks[*num_free - 1 - i]
+ *
+ * A sequence that finds too few blocks left (PA_DEVERR_FREE_LIST; no later sequence gets any
+ * either), would not fit its table row or has a negative length (PA_DEVERR_CONTEXT), or whose
+ * rows end past num_tokens (PA_DEVERR_QUERY) is not served: it keeps its length and table, and its
+ * rows get position 0 and slot -1.  The caller sees the reported bit and runs the step
+ * again with what it can serve.  A negative new length is reported (PA_DEVERR_QUERY) and taken as 0.
+ * A block id outside [0, num_blocks) is reported (PA_DEVERR_BLOCK_ID); its tokens get slot -1.
+ */
+int pa_tables_extend(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens, int32_t *query_start_loc,
+                     int32_t *positions, int64_t *slot_mapping, int num_tokens, int32_t *num_free_out,
+                     const int32_t *cached_lens, const int32_t *new_lens, int num_seqs, const int32_t *free_blocks,
+                     const int32_t *num_free, int free_capacity, int block_size, int num_blocks, int32_t *status,
+                     pa_stream_t stream);
+
+/*
+ * pa_tables_trim -- sequence s shrinks from cached_lens[s] to keep_lens[s] tokens (0: it has ended;
+ * a few fewer: drafted tokens were rejected).  The blocks it no longer needs, those from
+ * ceil(keep / block_size) on, go onto the stack, sequence by sequence, each sequence's last block
+ * first (so that a pa_tables_extend of one trimmed sequence gives it the same blocks again).
+ * free_blocks is written from *num_free on, context_lens (may be cached_lens itself) gets the
+ * kept lengths, num_free_out (may be num_free itself) the new count; block_tables is only read.
+ * A keep length outside [0, cached] or a cached length past the table row is reported
+ * (PA_DEVERR_CONTEXT) and its sequence left as it is.  Blocks past the end of the list are
+ * reported (PA_DEVERR_FREE_LIST) and dropped, block ids outside [0, num_blocks) reported
+ * (PA_DEVERR_BLOCK_ID) and listed as they are.
+ */
+int pa_tables_trim(int32_t *free_blocks, int free_capacity, int32_t *context_lens, int32_t *num_free_out,
+                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cached_lens,
+                   const int32_t *keep_lens, int num_seqs, const int32_t *num_free, int block_size, int num_blocks,
+                   int32_t *status, pa_stream_t stream);
+
+/*
+ * The same three calls with their arguments in one record (see pa_window_args).  In
+ * pa_tables_args, lens is new_lens or keep_lens; pa_tables_trim_args reads neither
+ * query_start_loc, positions, slot_mapping nor num_tokens.
+ */
+typedef struct {
+    void *out;
+    const void *query, *key_cache, *value_cache;
+    const int32_t *query_start_loc, *key_ranges, *block_tables, *context_lens;
+    int32_t *status;
+    pa_stream_t stream;
+    int32_t out_dtype, kv_dtype, num_tokens, max_query_len, max_blocks_per_seq, max_context_len;
+    int32_t num_seqs, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+    float scale;
+} pa_cross_args;
+
+typedef struct {
+    int32_t *block_tables, *context_lens, *query_start_loc, *positions;
+    int64_t *slot_mapping;
+    int32_t *free_blocks, *num_free_out;
+    const int32_t *cached_lens, *lens, *num_free;
+    int32_t *status;
+    pa_stream_t stream;
+    int32_t num_seqs, max_blocks_per_seq, num_tokens, free_capacity, block_size, num_blocks;
+} pa_tables_args;
+
+int pa_cross_attention_args(const pa_cross_args *args);
+int pa_tables_extend_args(const pa_tables_args *args);
+int pa_tables_trim_args(const pa_tables_args *args);
 
 /* Static description of a PA_* return code. */
 const char *pa_status_string(int code);

@@ -19,7 +19,11 @@ Operations (see ``include/pa.h`` for layouts, ownership and error behaviour):
 * ``pa_decode_window`` / ``pa_prefill_window`` -- the attention over a sliding window and the
   first tokens (sinks);
 * ``pa_reshape_and_cache_rope_axes`` -- a step's queries and keys rotated with several position
-  axes (``RopeAxes``, ``pa_rope_pair_axes``), keys and values written to their slots.
+  axes (``RopeAxes``, ``pa_rope_pair_axes``), keys and values written to their slots;
+* ``pa_cross_attention`` -- rows of any number per sequence over its whole cached context (an
+  encoder's states, images), each row within its own range of keys;
+* ``pa_tables_extend`` / ``pa_tables_trim`` -- block tables, row starts, positions and slots made on
+  the GPU from lengths, blocks taken from and given back to a free list in device memory.
 """
 from __future__ import annotations
 
@@ -35,6 +39,7 @@ __all__ = [
     "pa_prefill_chunk", "pa_copy_blocks", "pa_status_string", "pa_version", "library_path",
     "Rope", "pa_rope_yarn_freqs", "pa_reshape_and_cache_rope", "pa_decode_rope", "pa_decode_write",
     "pa_decode_window", "pa_prefill_window", "RopeAxes", "pa_rope_pair_axes", "pa_reshape_and_cache_rope_axes",
+    "pa_cross_attention", "pa_tables_extend", "pa_tables_trim",
     "PA_F32", "PA_F16", "PA_BF16",
 ]
 
@@ -88,11 +93,14 @@ def _send(name: str, f, record: struct.Struct, *fields) -> None:
         raise PAError(rc, name)
 
 
-# The windowed and multi-axis calls go over as one packed record each (pa_window_args,
-# pa_rope_axes_args): ctypes takes about as long for their twenty arguments as the launch does.
+# The windowed, multi-axis, cross and table calls go over as one packed record each (pa_window_args,
+# pa_rope_axes_args, pa_cross_args, pa_tables_args): ctypes takes about as long for their twenty arguments as the launch does.
 _WINDOW_ARGS = struct.Struct("@9P14if4x")
 _ROPE_AXES_ARGS = struct.Struct("@12P3q10i")
-for _name in ("pa_decode_window_args", "pa_prefill_window_args", "pa_reshape_and_cache_rope_axes_args"):
+_CROSS_ARGS = struct.Struct("@10P12if4x")
+_TABLES_ARGS = struct.Struct("@12P6i")
+for _name in ("pa_decode_window_args", "pa_prefill_window_args", "pa_reshape_and_cache_rope_axes_args",
+              "pa_cross_attention_args", "pa_tables_extend_args", "pa_tables_trim_args"):
     getattr(_lib, _name).argtypes = [ctypes.c_char_p]
     getattr(_lib, _name).restype = _i32
 _lib.pa_rope_pair_axes.argtypes = [_vp, _i32, _vp, _i32, _i32]
@@ -455,3 +463,106 @@ def pa_reshape_and_cache_rope_axes(query_out, query, key, value, key_cache, valu
         rope.freqs.data_ptr(), rope.pair_axis.data_ptr(), 0 if status is None else status.data_ptr(),
         _current_stream(dev) if stream is None else _stream(stream), q_stride, k_stride, v_stride, T, Hq, Hkv, D,
         bs, NB, code, rope.rope_dim, rope.num_axes, rope.halves)
+
+
+# ----------------------------------------------------------------------------- cross attention
+
+def pa_cross_attention(out, query, query_start_loc, max_query_len: int, key_cache, value_cache, block_tables,
+                       context_lens, max_context_len: int, scale: float, *, key_ranges=None, status=None,
+                       stream=None) -> None:
+    """out ``[T][Hq][D]`` = attention of query ``[T][Hq][D]`` over each sequence's whole cached context.
+    ``query_start_loc`` (int32 [S + 1]) gives each sequence's rows; None: one row per sequence.
+    ``key_ranges`` (int32 [T][2]): row t sees the keys from ``[t][0]`` up to, not including, ``[t][1]``."""
+    what = "pa_cross_attention"
+    (T, Hq, D), (NB, bs, Hkv, _), width, code, dev = _check_window(
+        what, out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, status)
+    if key_ranges is not None:
+        if key_ranges.dtype is not torch.int32 or key_ranges.shape != (T, 2) or not key_ranges.is_contiguous():
+            _refuse(what, "key_ranges is int32 [T][2], contiguous")
+        if key_ranges.get_device() != dev:
+            _refuse(what, "tensors must be on one CUDA device")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_cross_attention(out, query, query_start_loc, max_query_len, key_cache, value_cache, block_tables,
+                                      context_lens, max_context_len, scale, key_ranges=key_ranges, status=status,
+                                      stream=stream)
+    _send(what, _lib.pa_cross_attention_args, _CROSS_ARGS,
+        out.data_ptr(), query.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+        0 if query_start_loc is None else query_start_loc.data_ptr(), 0 if key_ranges is None else key_ranges.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), 0 if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream), _dt(out), code, T, max_query_len, width,
+        max_context_len, context_lens.shape[0], Hq, Hkv, D, bs, NB, scale)
+
+
+# ----------------------------------------------------------------------------- tables on the GPU
+
+def _check_tables(what, block_tables, lens, int32s, status):
+    """Types, layout and device of the table calls' tensors (``lens``: [S] each); returns S, the
+    table's width and the device's index."""
+    i32, shape, dev = torch.int32, block_tables.shape, block_tables.get_device()
+    if len(shape) != 2 or any(len(t.shape) != 1 or t.shape[0] != shape[0] for t in lens):
+        _refuse(what, "block_tables is [S][max_blocks], lengths are [S]")
+    for t in (block_tables, *lens, *int32s):
+        if t.dtype is not i32 or not t.is_contiguous():
+            _refuse(what, "tensors are int32 (slot_mapping int64) and contiguous")
+        if t.get_device() != dev:
+            _refuse(what, "tensors must be on one CUDA device")
+    if status is not None and (status.dtype is not i32 or status.numel() < 1 or status.get_device() != dev):
+        _refuse(what, "status is int32 [1] on the tensors' device")
+    if dev < 0:
+        _refuse(what, "tensors must be on one CUDA device")
+    return shape[0], shape[1], dev
+
+
+def pa_tables_extend(block_tables, context_lens, query_start_loc, positions, slot_mapping, num_free_out, cached_lens,
+                     new_lens, free_blocks, num_free, block_size: int, num_blocks: int, *, status=None,
+                     stream=None) -> None:
+    """Sequences grow from ``cached_lens`` to ``cached_lens + new_lens`` tokens (int32 [S]): blocks taken
+    from the stack ``free_blocks[:num_free]`` enter ``block_tables`` [S][max_blocks]; ``context_lens`` [S],
+    ``query_start_loc`` [S + 1] and ``positions`` [T] (either may be None), ``slot_mapping`` (int64 [T], -1
+    behind the last token) and ``num_free_out`` [1] are written."""
+    what = "pa_tables_extend"
+    more = [t for t in (query_start_loc, positions) if t is not None]
+    S, width, dev = _check_tables(what, block_tables, (context_lens, cached_lens, new_lens),
+                                  (num_free_out, free_blocks, num_free, *more), status)
+    T = slot_mapping.numel()
+    if slot_mapping.dtype is not torch.int64 or len(slot_mapping.shape) != 1 or not slot_mapping.is_contiguous() or (
+            slot_mapping.get_device() != dev):
+        _refuse(what, "slot_mapping is int64 [T], contiguous, on the tensors' device")
+    if (query_start_loc is not None and query_start_loc.shape != (S + 1,)) or (
+            positions is not None and positions.shape != (T,)):
+        _refuse(what, "query_start_loc is [S + 1], positions are [T] as slot_mapping")
+    if num_free.numel() < 1 or num_free_out.numel() < 1 or len(free_blocks.shape) != 1:
+        _refuse(what, "num_free and num_free_out are [1], free_blocks is one list")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_tables_extend(block_tables, context_lens, query_start_loc, positions, slot_mapping, num_free_out,
+                                    cached_lens, new_lens, free_blocks, num_free, block_size, num_blocks,
+                                    status=status, stream=stream)
+    _send(what, _lib.pa_tables_extend_args, _TABLES_ARGS,
+        block_tables.data_ptr(), context_lens.data_ptr(), 0 if query_start_loc is None else query_start_loc.data_ptr(),
+        0 if positions is None else positions.data_ptr(), slot_mapping.data_ptr(), free_blocks.data_ptr(),
+        num_free_out.data_ptr(), cached_lens.data_ptr(), new_lens.data_ptr(), num_free.data_ptr(),
+        0 if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream), S,
+        width, T, free_blocks.shape[0], block_size, num_blocks)
+
+
+def pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached_lens, keep_lens, num_free,
+                   block_size: int, num_blocks: int, *, status=None, stream=None) -> None:
+    """Sequences shrink from ``cached_lens`` to ``keep_lens`` tokens (int32 [S]; 0: ended): the blocks that
+    they no longer need go onto the stack ``free_blocks`` behind its ``num_free`` entries; ``context_lens``
+    [S] and ``num_free_out`` [1] are written."""
+    what = "pa_tables_trim"
+    S, width, dev = _check_tables(what, block_tables, (context_lens, cached_lens, keep_lens),
+                                  (num_free_out, free_blocks, num_free), status)
+    if num_free.numel() < 1 or num_free_out.numel() < 1 or len(free_blocks.shape) != 1:
+        _refuse(what, "num_free and num_free_out are [1], free_blocks is one list")
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached_lens, keep_lens,
+                                  num_free, block_size, num_blocks, status=status, stream=stream)
+    _send(what, _lib.pa_tables_trim_args, _TABLES_ARGS,
+        block_tables.data_ptr(), context_lens.data_ptr(), 0, 0, 0, free_blocks.data_ptr(), num_free_out.data_ptr(),
+        cached_lens.data_ptr(), keep_lens.data_ptr(), num_free.data_ptr(), 0 if status is None else status.data_ptr(),
+        _current_stream(dev) if stream is None else _stream(stream), S, width, 0, free_blocks.shape[0], block_size,
+        num_blocks)

@@ -1,0 +1,15 @@
+// cross.cuh -- arguments and launchers of the attention over another sequence's states.
+#pragma once
+
+#include "common.cuh"
+
+namespace pa {
+
+struct CrossArgs {
+    PrefillArgs a;              // query_start_loc null: row s belongs to sequence s
+    const int32_t *key_ranges;  // [num_tokens][2] first key and one past the last, or null
+};
+
+int launch_cross(const CrossArgs &c);
+
+}  // namespace pa

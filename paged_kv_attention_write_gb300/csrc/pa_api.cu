@@ -6,7 +6,8 @@
 // nothing is synchronised here.
 #include <cmath>
 
-#include "common.cuh"
+#include "cross.cuh"
+#include "tables.cuh"
 
 namespace {
 
@@ -385,6 +386,104 @@ int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *a) {
                                           a->slot_mapping, a->positions, a->num_tokens, a->num_heads, a->num_kv_heads,
                                           a->head_dim, a->query_stride, a->key_stride, a->value_stride, a->block_size,
                                           a->num_blocks, (pa_dtype)a->kv_dtype, &rope, a->status, a->stream);
+}
+
+int pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, const int32_t *query_start_loc,
+                       int num_tokens, int max_query_len, const int32_t *key_ranges, const void *key_cache,
+                       const void *value_cache, const int32_t *block_tables, int max_blocks_per_seq,
+                       const int32_t *context_lens, int max_context_len, int num_seqs, int num_heads,
+                       int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+                       pa_dtype kv_dtype, int32_t *status, pa_stream_t stream) {
+    // no rows: nothing is read, and empty tensors have no address
+    const bool nothing = num_tokens == 0 || (query_start_loc && max_query_len == 0);
+    int rc = check_attention(out, out_dtype, query, key_cache, value_cache, block_tables,
+                             max_blocks_per_seq, context_lens, max_context_len,
+                             nothing && num_seqs > 0 ? 0 : num_seqs,
+                             num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                             kv_dtype);
+    if (rc != PA_OK) return rc;
+    if (num_tokens < 0 || max_query_len < 0 || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+    if (!query_start_loc && num_tokens != num_seqs) return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || nothing) return PA_OK;
+    if (!aligned(query_start_loc, 4) || !aligned(key_ranges, 8) || !aligned(status, 4)) return PA_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)num_blocks * block_size;
+    if (rows <= 0) return PA_ERR_INVALID_ARG;
+    pa::PrefillArgs a{out,          out_dtype,  query,        query_start_loc,   num_tokens,
+                      query_start_loc ? max_query_len : 1, key_cache, value_cache, block_tables, max_blocks_per_seq,
+                      context_lens, max_context_len, num_seqs, num_heads,        num_kv_heads,
+                      head_dim,     block_size, num_blocks,   scale,             kv_dtype,
+                      status,       reinterpret_cast<cudaStream_t>(stream)};
+    return pa::launch_cross(pa::CrossArgs{a, key_ranges});
+}
+
+int pa_cross_attention_args(const pa_cross_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    return pa_cross_attention(a->out, (pa_dtype)a->out_dtype, a->query, a->query_start_loc, a->num_tokens,
+                              a->max_query_len, a->key_ranges, a->key_cache, a->value_cache, a->block_tables,
+                              a->max_blocks_per_seq, a->context_lens, a->max_context_len, a->num_seqs, a->num_heads,
+                              a->num_kv_heads, a->head_dim, a->block_size, a->num_blocks, a->scale,
+                              (pa_dtype)a->kv_dtype, a->status, a->stream);
+}
+
+// What both table calls ask of their arguments; `tables` and `list` are what they read or write.
+static int check_tables(const pa_tables_args *a) {
+    if (a->num_seqs < 0 || a->num_seqs > 65535 || a->max_blocks_per_seq < 0 || a->free_capacity < 0 ||
+        a->free_capacity == INT32_MAX || a->num_blocks < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!block_size_ok(a->block_size)) return PA_ERR_UNSUPPORTED;
+    if ((int64_t)a->max_blocks_per_seq * a->block_size > INT32_MAX || (int64_t)a->num_blocks * a->block_size > INT32_MAX)
+        return PA_ERR_INVALID_ARG;
+    if (!a->num_free || !a->num_free_out || (a->free_capacity > 0 && !a->free_blocks)) return PA_ERR_INVALID_ARG;
+    if (a->num_seqs > 0 && (!a->context_lens || !a->cached_lens || !a->lens ||
+                            (a->max_blocks_per_seq > 0 && !a->block_tables)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(a->block_tables, 4) || !aligned(a->context_lens, 4) || !aligned(a->query_start_loc, 4) ||
+        !aligned(a->positions, 4) || !aligned(a->slot_mapping, 8) || !aligned(a->free_blocks, 4) ||
+        !aligned(a->num_free_out, 4) || !aligned(a->cached_lens, 4) || !aligned(a->lens, 4) ||
+        !aligned(a->num_free, 4) || !aligned(a->status, 4))
+        return PA_ERR_INVALID_ARG;
+    return PA_OK;
+}
+static pa::TablesArgs tables_args(const pa_tables_args *a) {
+    return {a->block_tables, a->context_lens, a->query_start_loc, a->positions, a->slot_mapping, a->free_blocks,
+            a->num_free_out, a->cached_lens, a->lens, a->num_free, a->num_seqs, a->max_blocks_per_seq, a->num_tokens,
+            a->free_capacity, a->block_size, a->num_blocks, a->status, reinterpret_cast<cudaStream_t>(a->stream)};
+}
+
+int pa_tables_extend_args(const pa_tables_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const int rc = check_tables(a);
+    if (rc != PA_OK) return rc;
+    if (a->num_tokens < 0 || a->num_tokens == INT32_MAX || (a->num_tokens > 0 && !a->slot_mapping))
+        return PA_ERR_INVALID_ARG;
+    return pa::launch_tables_extend(tables_args(a));
+}
+
+int pa_tables_trim_args(const pa_tables_args *a) {
+    if (!a) return PA_ERR_INVALID_ARG;
+    const int rc = check_tables(a);
+    return rc != PA_OK ? rc : pa::launch_tables_trim(tables_args(a));
+}
+
+int pa_tables_extend(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens, int32_t *query_start_loc,
+                     int32_t *positions, int64_t *slot_mapping, int num_tokens, int32_t *num_free_out,
+                     const int32_t *cached_lens, const int32_t *new_lens, int num_seqs, const int32_t *free_blocks,
+                     const int32_t *num_free, int free_capacity, int block_size, int num_blocks, int32_t *status,
+                     pa_stream_t stream) {
+    const pa_tables_args a{block_tables, context_lens, query_start_loc, positions, slot_mapping,
+                           const_cast<int32_t *>(free_blocks), num_free_out, cached_lens, new_lens, num_free, status,
+                           stream, num_seqs, max_blocks_per_seq, num_tokens, free_capacity, block_size, num_blocks};
+    return pa_tables_extend_args(&a);
+}
+
+int pa_tables_trim(int32_t *free_blocks, int free_capacity, int32_t *context_lens, int32_t *num_free_out,
+                   const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cached_lens,
+                   const int32_t *keep_lens, int num_seqs, const int32_t *num_free, int block_size, int num_blocks,
+                   int32_t *status, pa_stream_t stream) {
+    const pa_tables_args a{const_cast<int32_t *>(block_tables), context_lens, nullptr, nullptr, nullptr, free_blocks,
+                           num_free_out, cached_lens, keep_lens, num_free, status, stream, num_seqs,
+                           max_blocks_per_seq, 0, free_capacity, block_size, num_blocks};
+    return pa_tables_trim_args(&a);
 }
 
 }  // extern "C"
