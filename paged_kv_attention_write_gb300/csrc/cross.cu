@@ -107,6 +107,8 @@ int launch_typed(const Params &p) {
 }  // namespace
 
 int launch_cross(const CrossArgs &c) {
+    const int G = c.a.num_heads / c.a.num_kv_heads;
+    if (c.a.kv_dtype != PA_F32 && c.a.query_start_loc && (int64_t)c.a.max_query_len * G > 8) return launch_cross_chunk(c);
     const Params p{c.a, c.key_ranges};
     switch (c.a.kv_dtype) {
         case PA_F32: return launch_typed<F32>(p);

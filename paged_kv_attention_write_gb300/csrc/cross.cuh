@@ -11,5 +11,6 @@ struct CrossArgs {
 };
 
 int launch_cross(const CrossArgs &c);
+int launch_cross_chunk(const CrossArgs &c);  // 16-bit caches, query_start_loc given
 
 }  // namespace pa
