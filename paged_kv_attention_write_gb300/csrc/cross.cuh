@@ -12,5 +12,6 @@ struct CrossArgs {
 
 int launch_cross(const CrossArgs &c);
 int launch_cross_chunk(const CrossArgs &c);  // 16-bit caches, query_start_loc given
+int load_cross_chunk(pa_dtype dtype, int head_dim);
 
 }  // namespace pa

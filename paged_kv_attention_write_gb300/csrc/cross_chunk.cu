@@ -5,6 +5,11 @@
 
 namespace pa {
 
+int load_cross_chunk(pa_dtype dtype, int head_dim) {
+    if (dtype == PA_F16) return head_dim == 64 ? load_typed<F16, 64, true>() : load_typed<F16, 128, true>();
+    return head_dim == 64 ? load_typed<BF16, 64, true>() : load_typed<BF16, 128, true>();
+}
+
 int launch_cross_chunk(const CrossArgs &c) { return launch_rows<true>(c.a, c.key_ranges); }
 
 }  // namespace pa

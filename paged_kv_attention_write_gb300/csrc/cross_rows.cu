@@ -1,0 +1,96 @@
+// cross_rows.cu -- few query rows over another sequence's whole paged context, each within its own
+// range of keys (kernels: stream_rows.cuh), and the choice between them and the chunks' kernel.
+#include "cross.cuh"
+#include "stream_rows.cuh"
+
+namespace pa {
+namespace {
+
+int launch_cross_rows(const CrossArgs &c) {
+    const PrefillArgs &a = c.a;
+    Params p{};
+    p.out = a.out;
+    p.out_dtype = a.out_dtype;
+    p.query = a.query;
+    p.block_tables = a.block_tables;
+    p.context_lens = a.context_lens;
+    p.max_blocks_per_seq = a.max_blocks_per_seq;
+    p.max_context_len = a.max_context_len;
+    p.num_heads = a.num_heads;
+    p.num_kv_heads = a.num_kv_heads;
+    p.group = a.num_heads / a.num_kv_heads;
+    p.block_size = a.block_size;
+    p.num_blocks = a.num_blocks;
+    p.qk_scale_log2 = a.scale * kLog2e;
+    p.status = a.status;
+    p.query_start_loc = a.query_start_loc;
+    p.key_ranges = c.key_ranges;
+    p.num_tokens = a.num_tokens;
+    p.max_query_len = a.max_query_len;
+    p.num_seqs = a.num_seqs;
+    p.group_log2 = p.group == 1 ? 0 : p.group == 2 ? 1 : p.group == 4 ? 2 : 3;
+    p.tokens = 1;
+    const int longest = std::min(a.max_query_len, a.num_tokens);
+    while (p.tokens < longest && p.tokens * p.group < 8) p.tokens *= 2;
+    p.token_groups = (longest - 1) / p.tokens + 1;
+    const int columns = p.tokens * p.group;
+    // Clusters as in decode_window.cu: the CTAs of one full wave, none with less than one stage of
+    // keys (two past eight CTAs).
+    const int sms = std::max(1, device_sm_count());
+    const int64_t slots = 2 * sms, most = a.max_context_len;
+    const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
+    const int64_t items = (int64_t)a.num_seqs * p.token_groups * a.num_kv_heads;
+    auto fit = [&](int size) { return slots * (size <= 2 ? 64 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
+    int cluster = 1;
+    while (cluster < 16 && items * cluster * 2 <= fit(cluster * 2) &&
+           most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
+        cluster *= 2;
+    p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
+    const int per_sm = (int)std::min<int64_t>(8, (items + sms - 1) / sms);
+    const bool by_warp = a.kv_dtype != PA_F32 && items > slots && most <= (per_sm * a.head_dim >= 320 ? 1152 : 384);
+    const int warps = by_warp ? per_sm : 0;
+    if (by_warp) p.unit = a.block_size >= 16 && most >= a.head_dim * per_sm ? 2 : 1;
+    if (items * cluster > INT32_MAX) return PA_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)(items * cluster));
+    const int64_t rows = (int64_t)a.num_blocks * a.block_size;
+    CUtensorMap km, vm;
+    for (int i = 0; i < 2; ++i) {
+        CUtensorMap *m = i ? &vm : &km;
+        const void *base = i ? a.value_cache : a.key_cache;
+        const int rc = a.kv_dtype == PA_F32
+                           ? make_kv_tensor_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 1, 8 * p.unit)
+                           : make_kv_block_map(m, base, a.kv_dtype, a.head_dim, a.num_kv_heads, rows, 8 * p.unit);
+        if (rc != PA_OK) return rc;
+    }
+    switch (a.kv_dtype) {
+        case PA_F32:
+            return a.head_dim == 64 ? launch_f32<64, true>(p, cluster, grid, columns, km, vm, a.stream)
+                                    : launch_f32<128, true>(p, cluster, grid, columns, km, vm, a.stream);
+        case PA_F16:
+            return a.head_dim == 64 ? launch_16<F16, 64, true>(p, cluster, grid, items, warps, km, vm, a.stream)
+                                    : launch_16<F16, 128, true>(p, cluster, grid, items, warps, km, vm, a.stream);
+        case PA_BF16:
+            return a.head_dim == 64 ? launch_16<BF16, 64, true>(p, cluster, grid, items, warps, km, vm, a.stream)
+                                    : launch_16<BF16, 128, true>(p, cluster, grid, items, warps, km, vm, a.stream);
+    }
+    return PA_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+int launch_cross(const CrossArgs &c) {
+    const PrefillArgs &a = c.a;
+    if (a.kv_dtype == PA_F32) return launch_cross_rows(c);
+    // Every kernel that a call with this type and head dimension may take is loaded by the first one on
+    // a device, so that any later one may be captured.
+    const bool half = a.kv_dtype == PA_F16, wide = a.head_dim == 128;
+    int rc = half ? (wide ? load_16<F16, 128, true>() : load_16<F16, 64, true>())
+                  : (wide ? load_16<BF16, 128, true>() : load_16<BF16, 64, true>());
+    if (rc == PA_OK) rc = load_cross_chunk(a.kv_dtype, a.head_dim);
+    if (rc != PA_OK) return rc;
+    // The rows' kernel has eight columns, the chunks' a tile of 128.
+    const int G = a.num_heads / a.num_kv_heads;
+    return (int64_t)a.max_query_len * G <= 8 ? launch_cross_rows(c) : launch_cross_chunk(c);
+}
+
+}  // namespace pa

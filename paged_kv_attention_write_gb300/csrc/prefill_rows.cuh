@@ -1019,22 +1019,29 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     }
 }
 
+// Both kernels are loaded by a device's first call, so that a captured call of other sizes
+// than the eager ones before it loads nothing.
+template <class T, int D, bool CROSS>
+int load_typed() {
+    constexpr int SMEM = CROSS ? Shape<D>::SMEM_CROSS : Shape<D>::SMEM;
+    static std::atomic<int> loaded[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices && loaded[dev].load(std::memory_order_acquire)) return PA_OK;
+    for (auto kernel : {prefill_rows_kernel<T, D, false, CROSS>, prefill_rows_kernel<T, D, true, CROSS>})
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
+            return PA_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices) loaded[dev].store(1, std::memory_order_release);
+    return PA_OK;
+}
+
 template <class T, int D, bool CROSS>
 int launch_typed(const Params &p, int64_t items, int cluster, const CUtensorMap &qm, const CUtensorMap &km,
                  const CUtensorMap &vm, cudaStream_t st) {
     constexpr int SMEM = CROSS ? Shape<D>::SMEM_CROSS : Shape<D>::SMEM;
     static std::atomic<int> whole_ready[kMaxDevices], split_ready[kMaxDevices];  // shared-memory limit raised
-    // Both kernels are loaded by a device's first call, so that a captured call of other sizes
-    // than the eager ones before it loads nothing.
-    static std::atomic<int> loaded[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-    if (dev < 0 || dev >= kMaxDevices || !loaded[dev].load(std::memory_order_acquire)) {
-        for (auto kernel : {prefill_rows_kernel<T, D, false, CROSS>, prefill_rows_kernel<T, D, true, CROSS>})
-            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
-                return PA_ERR_CUDA;
-        if (dev >= 0 && dev < kMaxDevices) loaded[dev].store(1, std::memory_order_release);
-    }
+    const int rc = load_typed<T, D, CROSS>();
+    if (rc != PA_OK) return rc;
     const dim3 grid((unsigned)(items * cluster)), block(kThreads);
     const cudaError_t e = cluster > 1 ? launch_pdl_cluster(prefill_rows_kernel<T, D, true, CROSS>, split_ready, grid, block,
                                                            SMEM, cluster, st, qm, km, vm, p)
