@@ -496,22 +496,31 @@ def pa_cross_attention(out, query, query_start_loc, max_query_len: int, key_cach
 
 # ----------------------------------------------------------------------------- tables on the GPU
 
-def _check_tables(what, block_tables, lens, int32s, status):
-    """Types, layout and device of the table calls' tensors (``lens``: [S] each); returns S, the
-    table's width and the device's index."""
-    i32, shape, dev = torch.int32, block_tables.shape, block_tables.get_device()
-    if len(shape) != 2 or any(len(t.shape) != 1 or t.shape[0] != shape[0] for t in lens):
-        _refuse(what, "block_tables is [S][max_blocks], lengths are [S]")
-    for t in (block_tables, *lens, *int32s):
-        if t.dtype is not i32 or not t.is_contiguous():
-            _refuse(what, "tensors are int32 (slot_mapping int64) and contiguous")
-        if t.get_device() != dev:
-            _refuse(what, "tensors must be on one CUDA device")
+_TABLES_TYPES = "tensors are int32 (slot_mapping int64) and contiguous"
+_TABLES_SHAPES = "block_tables is [S][max_blocks], lengths are [S], query_start_loc [S + 1], counts [1], positions [T]"
+
+
+def _check_tables(what, tables, a, b, c, free, n_in, n_out, status):
+    """Types, layout, sizes and device of the tensors that both table calls take (``a``, ``b``, ``c``: lengths);
+    returns S, the table's width and the device's index.  Spelled out: the calls are a few
+    microseconds long, and a loop over the tensors costs one of them."""
+    i32, dev = torch.int32, tables.get_device()
+    if not (tables.dtype is i32 and a.dtype is i32 and b.dtype is i32 and c.dtype is i32 and free.dtype is i32 and
+            n_in.dtype is i32 and n_out.dtype is i32 and tables.is_contiguous() and a.is_contiguous() and
+            b.is_contiguous() and c.is_contiguous() and free.is_contiguous()):
+        _refuse(what, _TABLES_TYPES)
+    if not (dev >= 0 and a.get_device() == dev == b.get_device() == c.get_device() and free.get_device() == dev and
+            n_in.get_device() == dev == n_out.get_device()):
+        _refuse(what, "tensors must be on one CUDA device")
+    shape = tables.shape
+    if len(shape) != 2:
+        _refuse(what, _TABLES_SHAPES)
+    S, width = shape
+    if not (a.numel() == S == b.numel() == c.numel()) or n_in.numel() < 1 or n_out.numel() < 1:
+        _refuse(what, _TABLES_SHAPES)
     if status is not None and (status.dtype is not i32 or status.numel() < 1 or status.get_device() != dev):
         _refuse(what, "status is int32 [1] on the tensors' device")
-    if dev < 0:
-        _refuse(what, "tensors must be on one CUDA device")
-    return shape[0], shape[1], dev
+    return S, width, dev
 
 
 def pa_tables_extend(block_tables, context_lens, query_start_loc, positions, slot_mapping, num_free_out, cached_lens,
@@ -522,29 +531,36 @@ def pa_tables_extend(block_tables, context_lens, query_start_loc, positions, slo
     ``query_start_loc`` [S + 1] and ``positions`` [T] (either may be None), ``slot_mapping`` (int64 [T], -1
     behind the last token) and ``num_free_out`` [1] are written."""
     what = "pa_tables_extend"
-    more = [t for t in (query_start_loc, positions) if t is not None]
-    S, width, dev = _check_tables(what, block_tables, (context_lens, cached_lens, new_lens),
-                                  (num_free_out, free_blocks, num_free, *more), status)
+    S, width, dev = _check_tables(what, block_tables, context_lens, cached_lens, new_lens, free_blocks, num_free,
+                                  num_free_out, status)
     T = slot_mapping.numel()
-    if slot_mapping.dtype is not torch.int64 or len(slot_mapping.shape) != 1 or not slot_mapping.is_contiguous() or (
-            slot_mapping.get_device() != dev):
-        _refuse(what, "slot_mapping is int64 [T], contiguous, on the tensors' device")
-    if (query_start_loc is not None and query_start_loc.shape != (S + 1,)) or (
-            positions is not None and positions.shape != (T,)):
-        _refuse(what, "query_start_loc is [S + 1], positions are [T] as slot_mapping")
-    if num_free.numel() < 1 or num_free_out.numel() < 1 or len(free_blocks.shape) != 1:
-        _refuse(what, "num_free and num_free_out are [1], free_blocks is one list")
+    if slot_mapping.dtype is not torch.int64 or not slot_mapping.is_contiguous() or slot_mapping.get_device() != dev:
+        _refuse(what, _TABLES_TYPES)
+    starts = 0
+    if query_start_loc is not None:
+        if query_start_loc.dtype is not torch.int32 or not query_start_loc.is_contiguous() or (
+                query_start_loc.get_device() != dev):
+            _refuse(what, _TABLES_TYPES)
+        if query_start_loc.numel() != S + 1:
+            _refuse(what, _TABLES_SHAPES)
+        starts = query_start_loc.data_ptr()
+    at = 0
+    if positions is not None:
+        if positions.dtype is not torch.int32 or not positions.is_contiguous() or positions.get_device() != dev:
+            _refuse(what, _TABLES_TYPES)
+        if positions.numel() != T:
+            _refuse(what, _TABLES_SHAPES)
+        at = positions.data_ptr()
     if dev != _current_device():
         with torch.cuda.device(dev):
             return pa_tables_extend(block_tables, context_lens, query_start_loc, positions, slot_mapping, num_free_out,
                                     cached_lens, new_lens, free_blocks, num_free, block_size, num_blocks,
                                     status=status, stream=stream)
     _send(what, _lib.pa_tables_extend_args, _TABLES_ARGS,
-        block_tables.data_ptr(), context_lens.data_ptr(), 0 if query_start_loc is None else query_start_loc.data_ptr(),
-        0 if positions is None else positions.data_ptr(), slot_mapping.data_ptr(), free_blocks.data_ptr(),
+        block_tables.data_ptr(), context_lens.data_ptr(), starts, at, slot_mapping.data_ptr(), free_blocks.data_ptr(),
         num_free_out.data_ptr(), cached_lens.data_ptr(), new_lens.data_ptr(), num_free.data_ptr(),
         0 if status is None else status.data_ptr(), _current_stream(dev) if stream is None else _stream(stream), S,
-        width, T, free_blocks.shape[0], block_size, num_blocks)
+        width, T, free_blocks.numel(), block_size, num_blocks)
 
 
 def pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached_lens, keep_lens, num_free,
@@ -553,10 +569,8 @@ def pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached
     they no longer need go onto the stack ``free_blocks`` behind its ``num_free`` entries; ``context_lens``
     [S] and ``num_free_out`` [1] are written."""
     what = "pa_tables_trim"
-    S, width, dev = _check_tables(what, block_tables, (context_lens, cached_lens, keep_lens),
-                                  (num_free_out, free_blocks, num_free), status)
-    if num_free.numel() < 1 or num_free_out.numel() < 1 or len(free_blocks.shape) != 1:
-        _refuse(what, "num_free and num_free_out are [1], free_blocks is one list")
+    S, width, dev = _check_tables(what, block_tables, context_lens, cached_lens, keep_lens, free_blocks, num_free,
+                                  num_free_out, status)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached_lens, keep_lens,
@@ -564,5 +578,5 @@ def pa_tables_trim(free_blocks, context_lens, num_free_out, block_tables, cached
     _send(what, _lib.pa_tables_trim_args, _TABLES_ARGS,
         block_tables.data_ptr(), context_lens.data_ptr(), 0, 0, 0, free_blocks.data_ptr(), num_free_out.data_ptr(),
         cached_lens.data_ptr(), keep_lens.data_ptr(), num_free.data_ptr(), 0 if status is None else status.data_ptr(),
-        _current_stream(dev) if stream is None else _stream(stream), S, width, 0, free_blocks.shape[0], block_size,
+        _current_stream(dev) if stream is None else _stream(stream), S, width, 0, free_blocks.numel(), block_size,
         num_blocks)

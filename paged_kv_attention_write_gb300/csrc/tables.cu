@@ -10,9 +10,20 @@
 // (or a scratch array) between the prefix sums and what they address, and between reading
 // cached_lens and num_free and writing them in place.  Every CTA sums all sequences, 2048 at
 // a time, so that the CTAs exchange nothing but one barrier; then they share out the blocks and the
-// tokens, one per thread, each found by a binary search in the prefix sums in shared memory.
-// Sums saturate one past what they are compared with, so that no length overflows them.
+// tokens, each found by a binary search in the prefix sums in shared memory, four of a thread's
+// side by side.  Where every sequence has four at most (a decode step, rejected drafts), a
+// thread sees to its own sequences and nothing is searched.  Sums saturate one past what they are
+// compared with, so that no length overflows them.
+//
+// What bounds it is latency: the launch, the lengths, two barriers of the sums, a search (11 steps),
+// an entry of the list or the table, the store.  Measured in a replayed graph (us): 64 sequences of
+// one token each 3.9, 32 of 512 tokens 4.4 (11.2 in one CTA), 2048 of 0 to 60 tokens 7.4 (43.8 in one
+// CTA); blocks given back by 256 sequences that lose up to 8 tokens 3.6, by 512 ended of 1024 (132000
+// blocks) 7.6 (65.6 in one CTA).  One search at a time per thread took 8.8 and 17 us for the two large
+// ones; searches for single tokens of 2000 sequences 7.2 us (bank conflicts), a thread per
+// sequence 5.1.
 #include <algorithm>
+#include <type_traits>
 
 #include "cluster.cuh"
 #include "tables.cuh"
@@ -50,17 +61,44 @@ __device__ __forceinline__ Pair block_scan(Pair v, Pair cap, Pair (&warp_sums)[k
     return v;
 }
 
-// Largest i < n with at[i] <= x (at[0] <= x).
-__device__ __forceinline__ int last_not_past(const uint32_t *at, int n, uint32_t x) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (at[mid] <= x) lo = mid; else hi = mid;
-    }
-    return lo;
+// For each x: the largest i < n with at[i] <= x (at[0] <= x), F searches side by side.  What lies behind
+// at[n - 1] is read but not used.
+template <int F>
+__device__ __forceinline__ void last_not_past(const uint32_t *at, int n, const uint32_t (&x)[F], int (&i)[F]) {
+#pragma unroll
+    for (int u = 0; u < F; ++u) i[u] = 0;
+    auto steps = [&](auto first) {
+#pragma unroll
+        for (int step = decltype(first)::value; step; step >>= 1)
+#pragma unroll
+            for (int u = 0; u < F; ++u) {
+                const int j = i[u] + step;
+                const bool past = at[j] > x[u];
+                if (j < n && !past) i[u] = j;
+            }
+    };
+    if (n > 64) steps(std::integral_constant<int, kSlice / 2>{});
+    else steps(std::integral_constant<int, 32>{});
 }
 
 __device__ __forceinline__ int blocks_of(int tokens, int log2) { return (int)(((int64_t)tokens + (1 << log2) - 1) >> log2); }
+
+constexpr int kFlight = 4;  // blocks or tokens that a thread takes at once, so that their latencies overlap
+constexpr int kDirect = 4;  // blocks or tokens per sequence up to which each thread sees to its own
+
+// f(i, how many at once) over begin .. end - 1 by `stride` threads, this one the number `at`.
+template <class Fn>
+__device__ __forceinline__ void share_out(uint32_t begin, uint32_t end, uint32_t stride, uint32_t at, Fn f) {
+    for (uint32_t i = begin; i < end;) {
+        const bool rest = end - i <= stride;
+        if (i + at < end) {
+            if (rest) f(i + at, std::integral_constant<int, 1>{});
+            else f(i + at, std::integral_constant<int, kFlight>{});
+        }
+        if (rest || end - i <= kFlight * stride) break;
+        i += kFlight * stride;
+    }
+}
 
 // EXTEND: sequences grow by `lens` tokens.  Else they shrink to `lens` tokens.
 template <bool EXTEND>
@@ -106,8 +144,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs p, in
                 if (m < 0) err |= PA_DEVERR_QUERY;
                 if (c < 0 || (m >= 0 && (int64_t)c + m > room)) err |= PA_DEVERR_CONTEXT;
                 len[u] = max(m, 0);
+                valid[u] = valid[u] && len[u] > 0;
                 mine[u].rows = min((uint32_t)len[u], cap.rows);
-                mine[u].blocks = 0;  // set once it is known that its rows fit
+                mine[u].blocks = valid[u] ? min((uint32_t)(blocks_of(c + m, block_log2) - blocks_of(c, block_log2)), cap.blocks) : 0;
             } else {
                 valid[u] = c >= 0 && m >= 0 && m <= c && c <= room;
                 if (!valid[u]) err |= PA_DEVERR_CONTEXT;
@@ -116,34 +155,39 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs p, in
             }
             cached[u] = max(c, 0);
         }
-        uint32_t row_end[kPer];
-        if (EXTEND) {  // rows first: a sequence whose rows do not fit takes no blocks
+        // Both sums at once, as if all rows fitted; only if they do not, the blocks are summed again
+        // without the sequences whose rows end past num_tokens.
 #pragma unroll
-            for (int u = 0; u < kPer; ++u) sum.rows = min(sum.rows + mine[u].rows, cap.rows);
-            const Pair incl = block_scan(sum, cap, warp_sums);
-            // what lies before this thread's sequences: exact as long as it is not saturated
-            uint32_t at = __shfl_up_sync(kFullMask, incl.rows, 1);
+        for (int u = 0; u < kPer; ++u)
+            sum = {min(sum.rows + mine[u].rows, cap.rows), min(sum.blocks + mine[u].blocks, cap.blocks)};
+        const uint32_t before = carry.rows;
+        Pair incl = block_scan(sum, cap, warp_sums);
+        const uint32_t rows_end = min(before + warp_sums[kWarps - 1].rows, cap.rows);
+        carry.rows = rows_end;
+        uint32_t row_end[kPer];
+        if (EXTEND) {
+            uint32_t at = __shfl_up_sync(kFullMask, incl.rows, 1);  // rows before this thread's
             if (tid % 32 == 0) at = tid == 0 ? 0 : warp_sums[tid / 32 - 1].rows;
-            at = min(at + carry.rows, cap.rows);
+            at = min(at + before, cap.rows);
+            sum.blocks = 0;
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
                 const int i = tid * kPer + u;
                 if (i < n) starts[i] = min(at, most_rows);
                 at = min(at + mine[u].rows, cap.rows);
                 row_end[u] = at;
-                const bool fits = len[u] == 0 || at <= most_rows;
-                if (!fits) err |= PA_DEVERR_QUERY;
-                valid[u] = valid[u] && fits && len[u] > 0;
-                if (valid[u])
-                    mine[u].blocks = min((uint32_t)(blocks_of(cached[u] + len[u], block_log2) - blocks_of(cached[u], block_log2)), cap.blocks);
+                if (at > most_rows && len[u] > 0) {
+                    err |= PA_DEVERR_QUERY;
+                    valid[u] = false;
+                    mine[u].blocks = 0;
+                }
+                sum.blocks = min(sum.blocks + mine[u].blocks, cap.blocks);
             }
-            carry.rows = min(carry.rows + warp_sums[kWarps - 1].rows, cap.rows);
-            __syncthreads();
+            if (rows_end > most_rows) {  // the same for every thread
+                __syncthreads();
+                incl = block_scan(sum, cap, warp_sums);
+            }
         }
-        sum = {0, 0};
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) sum.blocks = min(sum.blocks + mine[u].blocks, cap.blocks);
-        const Pair incl = block_scan(sum, cap, warp_sums);
         uint32_t at = __shfl_up_sync(kFullMask, incl.blocks, 1);
         if (tid % 32 == 0) at = tid == 0 ? 0 : warp_sums[tid / 32 - 1].blocks;
         at = min(at + carry.blocks, cap.blocks);
@@ -169,11 +213,13 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs p, in
         }
         if (high > 0) atomicMax(&taken, high);
         const uint32_t first_block = carry.blocks;
-        const uint32_t rows_end = min(carry.rows, most_rows);  // of this slice
         carry.blocks = min(carry.blocks + warp_sums[kWarps - 1].blocks, cap.blocks);
         // Before anything is written in place, every CTA has read what it replaces.
+        bool many = false;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) many = many || (EXTEND ? (uint32_t)len[u] : mine[u].blocks) > kDirect;
         if (ranks > 1) cluster_sync();
-        __syncthreads();
+        const bool direct = !__syncthreads_or(many);
         if (rank == (base / kSlice) % ranks) {
 #pragma unroll
             for (int u = 0; u < kPer; ++u) {
@@ -183,40 +229,103 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs p, in
                 if (EXTEND && p.query_start_loc) p.query_start_loc[base + i + 1] = (int)min(row_end[u], most_rows);
             }
         }
-        // ---- blocks: number i of the call
-        for (uint32_t i = first_block + rank * kThreads + tid; i < min(taken, carry.blocks); i += ranks * kThreads) {
-            const int s = last_not_past(firsts, n, i);
-            const int c = cached_of[s] < 0 ? ~cached_of[s] : cached_of[s], have = blocks_of(c, block_log2);
-            const int64_t row = (int64_t)(base + s) * p.max_blocks_per_seq;
-            int id;
-            if (EXTEND) {
-                id = p.free_blocks[free0 - 1 - (int)i];
-                p.block_tables[row + have + (int)(i - firsts[s])] = id;
-            } else {
-                id = p.block_tables[row + have - 1 - (int)(i - firsts[s])];
-                p.free_blocks[free0 + (int)i] = id;
+        const uint32_t stride = ranks * kThreads;
+        // ---- few of them per sequence: each thread sees to its own sequences, the warps shared out
+        // over the CTAs (a search costs an access to a random bank per step)
+        if (direct) {
+            if (tid / 32 % ranks == rank) {
+#pragma unroll
+                for (int u = 0; u < kPer; ++u) {
+                    const int i = tid * kPer + u;
+                    if (i >= n) continue;
+                    const int have = blocks_of(cached[u], block_log2), first = (int)firsts[i];
+                    int32_t *row = p.block_tables + (int64_t)(base + i) * p.max_blocks_per_seq;
+                    if (EXTEND) {
+                        const int rows = min((int)(min(row_end[u], most_rows) - starts[i]), kDirect);
+                        for (int k = 0; k < rows; ++k) {
+                            const int pos = valid[u] ? cached[u] + k : 0, b = pos >> block_log2;
+                            int64_t slot = -1;
+                            if (valid[u]) {
+                                const int id = b < have ? row[b] : p.free_blocks[free0 - 1 - first - (b - have)];
+                                // a new block's first token enters it into the table
+                                if (b >= have && (k == 0 || (pos & ((1 << block_log2) - 1)) == 0)) row[b] = id;
+                                if (id >= 0 && id < p.num_blocks) slot = ((int64_t)id << block_log2) + (pos & ((1 << block_log2) - 1));
+                                else err |= PA_DEVERR_BLOCK_ID;
+                            }
+                            if (p.positions) p.positions[starts[i] + k] = pos;
+                            p.slot_mapping[starts[i] + k] = slot;
+                        }
+                    } else if (valid[u]) {
+                        for (int k = 0; k < (int)mine[u].blocks && first + k < (int)most_blocks; ++k) {
+                            const int id = row[have - 1 - k];
+                            p.free_blocks[free0 + first + k] = id;
+                            if (id < 0 || id >= p.num_blocks) err |= PA_DEVERR_BLOCK_ID;
+                        }
+                    }
+                }
             }
-            if (id < 0 || id >= p.num_blocks) err |= PA_DEVERR_BLOCK_ID;
+            __syncthreads();  // the next slice writes the shared arrays
+            continue;
         }
+        // ---- blocks: number i of the call
+        const uint32_t blocks_end = min(taken, carry.blocks);
+        auto blocks = [&](uint32_t i0, auto flight) {
+            constexpr int F = decltype(flight)::value;
+            uint32_t number[F];
+            int s[F], id[F];
+#pragma unroll
+            for (int u = 0; u < F; ++u) number[u] = min(i0 + u * stride, blocks_end - 1);
+            last_not_past<F>(firsts, n, number, s);
+            int32_t *entry[F];
+#pragma unroll
+            for (int u = 0; u < F; ++u) {
+                const int have = blocks_of(cached_of[s[u]], block_log2), k = (int)(number[u] - firsts[s[u]]);
+                entry[u] = p.block_tables + (int64_t)(base + s[u]) * p.max_blocks_per_seq + (EXTEND ? have + k : have - 1 - k);
+                id[u] = EXTEND ? p.free_blocks[free0 - 1 - (int)number[u]] : *entry[u];
+            }
+#pragma unroll
+            for (int u = 0; u < F; ++u) {
+                if (i0 + u * stride >= blocks_end) break;
+                if (EXTEND) *entry[u] = id[u];
+                else p.free_blocks[free0 + (int)number[u]] = id[u];
+                if (id[u] < 0 || id[u] >= p.num_blocks) err |= PA_DEVERR_BLOCK_ID;
+            }
+        };
+        share_out(first_block, blocks_end, stride, rank * kThreads + tid, blocks);
         // ---- tokens
         if (EXTEND) {
-            const uint32_t begin = starts[0];
-            for (uint32_t t = begin + rank * kThreads + tid; t < rows_end; t += ranks * kThreads) {
-                const int s = last_not_past(starts, n, t);
-                const int c = cached_of[s];
-                int64_t slot = -1;
-                int pos = 0;
-                if (c >= 0) {
-                    pos = c + (int)(t - starts[s]);
-                    const int b = pos >> block_log2, have = blocks_of(c, block_log2);
-                    const int id = b < have ? p.block_tables[(int64_t)(base + s) * p.max_blocks_per_seq + b]
-                                            : p.free_blocks[free0 - 1 - (int)firsts[s] - (b - have)];
-                    if (id >= 0 && id < p.num_blocks) slot = ((int64_t)id << block_log2) + (pos & ((1 << block_log2) - 1));
-                    else err |= PA_DEVERR_BLOCK_ID;
+            const uint32_t end = min(rows_end, most_rows);
+            auto tokens = [&](uint32_t t0, auto flight) {
+                constexpr int F = decltype(flight)::value;
+                uint32_t token[F];
+                int s[F], pos[F], id[F];
+                bool live[F];  // its sequence is served
+#pragma unroll
+                for (int u = 0; u < F; ++u) token[u] = min(t0 + u * stride, end - 1);
+                last_not_past<F>(starts, n, token, s);
+#pragma unroll
+                for (int u = 0; u < F; ++u) {
+                    const int c = cached_of[s[u]], first = (int)firsts[s[u]];
+                    live[u] = c >= 0;
+                    pos[u] = live[u] ? c + (int)(token[u] - starts[s[u]]) : 0;
+                    const int b = pos[u] >> block_log2, have = blocks_of(max(c, 0), block_log2);
+                    // its block: one that the sequence had, or one taken from the list
+                    const int32_t *from = b < have ? p.block_tables + (int64_t)(base + s[u]) * p.max_blocks_per_seq + b
+                                                   : p.free_blocks + (free0 - 1 - first - (b - have));
+                    id[u] = -1;
+                    if (live[u]) id[u] = *from;
                 }
-                if (p.positions) p.positions[t] = pos;
-                p.slot_mapping[t] = slot;
-            }
+#pragma unroll
+                for (int u = 0; u < F; ++u) {
+                    const uint32_t t = t0 + u * stride;
+                    if (t >= end) break;
+                    const bool ok = id[u] >= 0 && id[u] < p.num_blocks;
+                    if (live[u] && !ok) err |= PA_DEVERR_BLOCK_ID;
+                    if (p.positions) p.positions[t] = pos[u];
+                    p.slot_mapping[t] = ok ? ((int64_t)id[u] << block_log2) + (pos[u] & ((1 << block_log2) - 1)) : -1;
+                }
+            };
+            share_out(min(before, most_rows), end, stride, rank * kThreads + tid, tokens);
         }
         __syncthreads();  // the next slice writes the shared arrays
     }
@@ -234,11 +343,13 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs p, in
     if (err) report(p.status, err);
 }
 
+// `work`: tokens, or table entries of which some go back.  More CTAs than the work needs cost next to nothing
+// (one token of one sequence 4.1 us in one CTA, 4.3 in sixteen), fewer cost their share of it.
 template <bool EXTEND>
 int launch(const TablesArgs &a, int64_t work) {
     static std::atomic<int> ready[kMaxDevices];
     int cluster = 1;
-    while (cluster < 8 && work > (int64_t)kThreads * cluster) cluster *= 2;
+    while (cluster < 16 && work > (int64_t)kThreads * cluster) cluster *= 2;
     const int log2 = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
     return launch_pdl_cluster(tables_kernel<EXTEND>, ready, dim3(cluster), dim3(kThreads), 0, cluster, a.stream, a, log2) ==
                    cudaSuccess
@@ -249,6 +360,6 @@ int launch(const TablesArgs &a, int64_t work) {
 }  // namespace
 
 int launch_tables_extend(const TablesArgs &a) { return launch<true>(a, a.num_tokens); }
-int launch_tables_trim(const TablesArgs &a) { return launch<false>(a, (int64_t)a.num_seqs * 8); }
+int launch_tables_trim(const TablesArgs &a) { return launch<false>(a, (int64_t)a.num_seqs * a.max_blocks_per_seq); }
 
 }  // namespace pa
