@@ -31,24 +31,36 @@ int launch_cross_rows(const CrossArgs &c) {
     p.group_log2 = p.group == 1 ? 0 : p.group == 2 ? 1 : p.group == 4 ? 2 : 3;
     p.tokens = 1;
     const int longest = std::min(a.max_query_len, a.num_tokens);
-    while (p.tokens < longest && p.tokens * p.group < 8) p.tokens *= 2;
+    // fp32: a warp holds four columns, so eight take two warps per key and nothing is gained by sharing
+    // the keys (19 sequences of 1 to 3 rows of 4 heads 23.4 us with two rows to an item, 17.5 with one)
+    const int fill = a.kv_dtype == PA_F32 ? 4 : 8;
+    while (p.tokens < longest && p.tokens * p.group < fill) p.tokens *= 2;
     p.token_groups = (longest - 1) / p.tokens + 1;
     const int columns = p.tokens * p.group;
     // Clusters as in decode_window.cu: the CTAs of one full wave, none with less than one stage of
-    // keys (two past eight CTAs).
+    // keys (two past eight CTAs).  A ninth more than a wave still pays in twos where the contexts are
+    // ragged, which the host cannot see, and costs little where they are not (164 items of up to 1333
+    // fp32 keys 26.4 us whole, 17.5 in twos).
     const int sms = std::max(1, device_sm_count());
     const int64_t slots = 2 * sms, most = a.max_context_len;
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
     const int64_t items = (int64_t)a.num_seqs * p.token_groups * a.num_kv_heads;
-    auto fit = [&](int size) { return slots * (size <= 2 ? 64 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
+    // those that have rows: of ragged sequences some items are empty and gone at once
+    const int64_t live = std::min<int64_t>(items, (p.tokens == 1 ? a.num_tokens : a.num_tokens / p.tokens + (int64_t)a.num_seqs) *
+                                                      a.num_kv_heads);
+    auto fit = [&](int size) { return slots * (size == 2 ? 71 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
     int cluster = 1;
-    while (cluster < 16 && items * cluster * 2 <= fit(cluster * 2) &&
+    while (cluster < 16 && live * cluster * 2 <= fit(cluster * 2) &&
            most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
         cluster *= 2;
     p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
-    const int per_sm = (int)std::min<int64_t>(8, (items + sms - 1) / sms);
-    const bool by_warp = a.kv_dtype != PA_F32 && items > slots && most <= (per_sm * a.head_dim >= 320 ? 1152 : 384);
+    const int per_sm = (int)std::min<int64_t>(8, (live + sms - 1) / sms);
+    const bool by_warp = a.kv_dtype != PA_F32 && live > slots && most <= (per_sm * a.head_dim >= 320 ? 1152 : 384);
     const int warps = by_warp ? per_sm : 0;
+    // Long contexts first where a second wave of CTAs would otherwise end with one: 512 items of 1600
+    // to 6404 keys 194 -> 155 us, 800 of 500 to 2500 108 -> 97; past four waves the lengths even out
+    // and the ranking only costs (1600 items of 500 to 2500 keys 108 -> 114 us).
+    p.by_length = !by_warp && live * cluster > slots && live * cluster <= 4 * slots && a.num_seqs <= kMostRanked;
     if (by_warp) p.unit = a.block_size >= 16 && most >= a.head_dim * per_sm ? 2 : 1;
     if (items * cluster > INT32_MAX) return PA_ERR_INVALID_ARG;
     const dim3 grid((unsigned)(items * cluster));
@@ -88,9 +100,13 @@ int launch_cross(const CrossArgs &c) {
                   : (wide ? load_16<BF16, 128, true>() : load_16<BF16, 64, true>());
     if (rc == PA_OK) rc = load_cross_chunk(a.kv_dtype, a.head_dim);
     if (rc != PA_OK) return rc;
-    // The rows' kernel has eight columns, the chunks' a tile of 128.
-    const int G = a.num_heads / a.num_kv_heads;
-    return (int64_t)a.max_query_len * G <= 8 ? launch_cross_rows(c) : launch_cross_chunk(c);
+    // The rows' kernel has eight columns, the chunks' a tile of 128.  Above eight the keys are streamed once
+    // for every eight columns, which is still the faster as long as that fills the chip no more than
+    // clusters of eight CTAs do (one sequence of 4000 keys: 32 items 12.6 us, 15.3 on the chunks'
+    // kernel; 64 items 20.1 and 16.5).
+    const int64_t columns = (int64_t)std::min(a.max_query_len, a.num_tokens) * (a.num_heads / a.num_kv_heads);
+    const int64_t items = (int64_t)a.num_seqs * ((columns + 7) / 8) * a.num_kv_heads;
+    return columns <= 8 || items * 8 <= 2 * device_sm_count() ? launch_cross_rows(c) : launch_cross_chunk(c);
 }
 
 }  // namespace pa

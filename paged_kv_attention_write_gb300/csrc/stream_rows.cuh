@@ -80,6 +80,7 @@ struct Params {
     int num_tokens, max_query_len, num_seqs;
     int group_log2, tokens;  // tokens of an item; tokens << group_log2 is its columns, at most 8
     int token_groups;        // items of one kv head in the longest sequence
+    int by_length;           // sequences with long contexts first
 };
 
 template <class T, int D>
@@ -122,6 +123,8 @@ struct WindowKeys {
     }
 };
 
+constexpr int kMostRanked = 160;  // sequences that a CTA ranks by length: one per thread
+
 // An item of the cross attention (a kv head's columns of up to 8 tokens) and its keys.
 struct CrossKeys {
     int s, g, row0, rows;  // its query rows: row0 .. row0 + rows - 1
@@ -145,6 +148,26 @@ struct CrossKeys {
         const unsigned rest = number / (unsigned)p.num_kv_heads;
         const int part = (int)(rest % (unsigned)p.token_groups), first = part * p.tokens;
         s = (int)(rest / (unsigned)p.token_groups);
+        if (p.by_length) {  // the sequence of rank s (a thread each)
+            // length and number in one key, so that a comparison ranks two sequences (lengths from 2^22
+            // on count as alike: the order is only a matter of time)
+            __shared__ __align__(16) int order[kMostRanked];
+            const int i = (int)threadIdx.x;
+            const int key = i < p.num_seqs ? min(max(p.context_lens[i], 0), (1 << 22) - 1) << 8 | i : -1;
+            if (i < kMostRanked) order[i] = key;
+            __syncthreads();
+            if (i < p.num_seqs) {
+                int rank = 0;
+                for (int j = 0; j < p.num_seqs; j += 4) {
+                    const int4 x = *reinterpret_cast<const int4 *>(order + j);
+                    rank += (x.x > key) + (x.y > key) + (x.z > key) + (x.w > key);
+                }
+                if (rank == s) shared[0].x = i;
+            }
+            __syncthreads();
+            s = shared[0].x;
+            __syncthreads();  // the ranges go there next
+        }
         rep = rep && g == 0 && part == 0;
         int q0 = s, q1 = s + 1;
         if (p.query_start_loc) {
@@ -322,8 +345,8 @@ struct Consumer16 {
                                           uint32_t valid) {
         bool wrote = false;
 #pragma unroll
-        for (int step = 0; step < Sh::NGRP / 8; ++step) {
-            const int g0 = step * 8 + warp * 2;  // this warp's two groups of the stage
+        for (int step = 0; step < Sh::NGRP / (2 * Sh::NW); ++step) {
+            const int g0 = (step * Sh::NW + warp) * 2;  // this warp's two groups of the stage
             if (!(valid >> g0 & 3u)) continue;
             wrote |= pair(p, keys, kbase + g0 * Sh::GROUP_BYTES, vbase + g0 * Sh::GROUP_BYTES, first + g0,
                           valid >> g0 & 3u);
