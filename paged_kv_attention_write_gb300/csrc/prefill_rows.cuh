@@ -72,6 +72,7 @@ constexpr float kGrowLog2 = 8.f;
 // range: it has no bits below 2^-24, and a weight is at most 2^(8 + 7), of 2^16.
 template <class T>
 constexpr float kLiftLog2 = std::is_same<T, F16>::value ? 7.f : 0.f;
+constexpr int kMostRanked = 256;     // sequences whose items are ordered by length
 constexpr int kPlanSeqs = 2047;      // sequences whose items are listed without gaps
 
 struct Params {
@@ -87,6 +88,7 @@ struct Params {
     int32_t *status;
     const int32_t *key_ranges;  // cross attention: [num_tokens][2], or null
     int max_query_len;
+    int by_length;  // cross attention: the sequences with long contexts first
 };
 
 // r += the two weights packed in w, each widened exactly inside the add (mixed-precision add).
@@ -406,13 +408,33 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
     // CTAs are numbered sequence by sequence (the items of one share their keys in L2), from a
     // chunk's last rows to its first (the first rows of a fresh prompt see few keys), kv heads
     // side by side.
+    int *order = plan_mem + 2 * kMostRanked;  // CROSS, by_length: the sequences from the shortest context to the longest
+    if (CROSS && p.by_length) {
+        // length and number in one key, so that a comparison ranks two sequences (lengths from 2^22 on
+        // count as alike: the order is only a matter of time)
+        int *keys = plan_mem + 3 * kMostRanked;
+        for (int i = tid; i < kMostRanked; i += kThreads)
+            keys[i] = i < p.num_seqs ? min(max(p.context_lens[i], 0), (1 << 22) - 1) << 8 | i : INT32_MAX;
+        __syncthreads();
+        for (int i = tid; i < p.num_seqs; i += kThreads) {
+            const int key = keys[i];
+            int rank = 0;
+            for (int j = 0; j < p.num_seqs; j += 4) {
+                const int4 x = *reinterpret_cast<const int4 *>(keys + j);
+                rank += (x.x < key) + (x.y < key) + (x.z < key) + (x.w < key);
+            }
+            order[rank] = i;
+        }
+        __syncthreads();
+    }
     if (p.listed) {  // prefix sums of the sequences' units
         for (int i = tid; i <= p.num_seqs; i += kThreads) {
             int units = 0, ctx;
             if (i < p.num_seqs) {
-                const int q0 = p.query_start_loc[i], q1 = p.query_start_loc[i + 1];
-                if (CROSS ? cross_sequence(p, q0, q1, p.context_lens[i], true, ctx)
-                          : sequence(p, q0, q1, p.context_lens[i], true, ctx))
+                const int s = CROSS && p.by_length ? order[i] : i;
+                const int q0 = p.query_start_loc[s], q1 = p.query_start_loc[s + 1];
+                if (CROSS ? cross_sequence(p, q0, q1, p.context_lens[s], true, ctx)
+                          : sequence(p, q0, q1, p.context_lens[s], true, ctx))
                     units = min((q1 - q0 - 1) / (kBM >> p.group_log2) + 1, p.units_per_seq);
             }
             plan_mem[i] = units;
@@ -450,7 +472,15 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
         } else {
             seq = idx / p.units_per_seq;
             unit = p.units_per_seq - 1 - idx % p.units_per_seq;
+            if (CROSS && p.by_length) {
+                if (p.key_ranges) {  // the last rows, which may see most, of all sequences first
+                    unit = p.units_per_seq - 1 - idx / p.num_seqs;
+                    seq = idx % p.num_seqs;
+                }
+                seq = p.num_seqs - 1 - seq;
+            }
         }
+        if (CROSS && p.by_length) seq = order[seq];
         return make_item(p, seq, unit, g, rep && !p.listed && unit == 0 && g == 0, it);
     };
     It it{};
@@ -1083,6 +1113,7 @@ int launch_rows(const PrefillArgs &a, const int32_t *key_ranges) {
     const int64_t most = a.num_tokens / (kBM / G) + (int64_t)a.num_seqs;
     p.listed = a.num_seqs <= kPlanSeqs && most < uniform;
     const int64_t items = (p.listed ? most : uniform) * a.num_kv_heads;
+    p.by_length = CROSS && a.num_seqs > 1 && a.num_seqs <= kMostRanked;
     // Few items: a cluster of CTAs takes each, up to one CTA per SM and at least four key tiles
     // per CTA (the join costs about one tile's time).  45 rows of 8 heads behind 4096 keys: 45.0
     // us whole, 13.9 in eights, 12.8 in sixteens; of 32 heads behind 512 keys: 11.7 whole, 9.6
