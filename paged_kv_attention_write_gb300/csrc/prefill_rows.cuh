@@ -262,6 +262,7 @@ struct CrossItem {
     int sh;             // logical key of virtual key v: v + sh (a whole number of blocks)
     int blocks, tiles;  // virtual blocks, key tiles (one, all masked, where no row sees anything)
     int low, high;      // every row sees all keys of the tiles low .. high - 1
+    int holes;          // there may be keys of [lo, hi) that no row sees
 };
 
 // The keys [x, y) of the token at `tok + i` of an item's chunk (past the chunk's end: of its last token);
@@ -284,7 +285,7 @@ __device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int 
     it.Lq = q1 - q0;
     it.tok = unit * tt;
     if (!ok || unit < 0 || it.tok >= it.Lq) return false;
-    int lo = INT32_MAX, hi = 0, lo_in = 0, hi_in = INT32_MAX;
+    int lo = INT32_MAX, hi = 0, lo_in = 0, hi_in = INT32_MAX, last = 0, first = INT32_MAX;
     for (int i = lane; i < tt; i += 32) {
         const int2 r = row_range(p, it, i);
         const bool none = r.x >= r.y;
@@ -292,7 +293,11 @@ __device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int 
         hi = max(hi, none ? 0 : r.y);
         lo_in = max(lo_in, none ? INT32_MAX : r.x);
         hi_in = min(hi_in, none ? 0 : r.y);
+        last = max(last, none ? 0 : r.x);
+        first = min(first, none ? INT32_MAX : r.y);
     }
+    // ranges that reach from before the last begin to past the first end leave nothing out
+    it.holes = __reduce_max_sync(kFullMask, last) > __reduce_min_sync(kFullMask, first);
     hi = __reduce_max_sync(kFullMask, hi);
     lo = min(hi, __reduce_min_sync(kFullMask, lo));
     lo_in = __reduce_max_sync(kFullMask, lo_in);
@@ -313,6 +318,7 @@ __device__ __forceinline__ bool make_item(const Params &p, int s, int unit, int 
 __device__ __forceinline__ uint64_t seen_keys(const Params &p, const CrossItem &it, const int2 *ranges, int k0) {
     const int tt = kBM >> p.group_log2, lane = threadIdx.x % 32;
     auto below = [](int n) { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+    if (!it.holes) return below(it.hi - it.sh - k0) & ~below(it.lo - it.sh - k0);
     uint64_t seen = 0;
     for (int i = lane; i < tt; i += 32) {
         const int2 r = ranges[i];
@@ -600,7 +606,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             // CROSS: between the ranges of an item's rows there may be blocks that no row reaches
             auto reached = [&](int j) {
                 if constexpr (CROSS) {
-                    if (!p.key_ranges || (j0 + j >= it.low && j0 + j < it.high) || j >= n) return true;
+                    if (!it.holes || (j0 + j >= it.low && j0 + j < it.high) || j >= n) return true;
                     const uint64_t seen = seen_keys(p, it, row_ranges + (k & 1) * kBM, (j0 + j) * kBN);
                     return lane < nb && (seen >> (lane << bl) & ((1ull << (1 << bl)) - 1)) != 0;
                 }
@@ -721,7 +727,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                             sts128(sV + (r / 8) * Sh::GSTR + (rest / 8) * 1024 + (r % 8) * 128 + (rest % 8) * 16, 0u, 0u,
                                    0u, 0u);
                         }
-                    fence_async_smem();
+                    if (!CROSS || seen != ~0ull) fence_async_smem();
                     __syncwarp();
                 }
                 if (lane == 0) {
@@ -760,27 +766,65 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;  // l: this lane's share
             for (int t = 0; ok && t < n; ++t) {
                 const int sb = (done + t) % kSBufs;
+                // CROSS: the keys of the tile that this thread's two rows see, and whether some row of the warp sees
+                // a part of it
+                int lo0 = 0, hi0 = kBN, lo1 = 0, hi1 = kBN;
+                bool parts = false, blind = false;
+                if constexpr (CROSS) {
+                    if (j0 + t < low || j0 + t >= high) {
+                        const int2 *ranges = row_ranges + (SPLIT ? 0 : (k & 1) * kBM);
+                        const int k0 = cur.sh + (j0 + t) * kBN;
+                        const int2 r0 = ranges[row0 >> p.group_log2], r1 = ranges[row1 >> p.group_log2];
+                        lo0 = max(r0.x - k0, 0);
+                        hi0 = min(r0.y - k0, kBN);
+                        lo1 = max(r1.x - k0, 0);
+                        hi1 = min(r1.y - k0, kBN);
+                        const bool none0 = lo0 >= hi0, none1 = lo1 >= hi1;
+                        blind = __all_sync(kFullMask, none0 && none1);
+                        parts = __any_sync(kFullMask, (!none0 && (lo0 > 0 || hi0 < kBN)) || (!none1 && (lo1 > 0 || hi1 < kBN)));
+                    }
+                }
                 ok = __all_sync(kFullMask, wait(BSF + sb, (done + t) / kSBufs));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t tS = tL + sb * kBN;
+                // the tile is for other rows of the item (half of the rows of every item blind to all tiles but the
+                // first: 290 us with their scores masked one by one, 187 where all rows see all)
+                if (CROSS && blind) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = 0u;
+                    tmem_st_16x128b_x8(tS, w);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(BPF + sb));
+                    continue;
+                }
                 uint32_t s[32];
                 tmem_ld_16x256b<8>(tS, s);
                 tmem_wait_ld();
                 if (j0 + t < low || j0 + t >= high) {
                     if constexpr (CROSS) {
-                        const int2 *ranges = row_ranges + (SPLIT ? 0 : (k & 1) * kBM);
-                        const int k0 = cur.sh + (j0 + t) * kBN;
-                        const int2 r0 = ranges[row0 >> p.group_log2], r1 = ranges[row1 >> p.group_log2];
-                        const int lo0 = r0.x - k0, hi0 = r0.y - k0, lo1 = r1.x - k0, hi1 = r1.y - k0;
+                        if (parts) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = 8 * i + 2 * ga + e;
-                                if (key < lo0 || key >= hi0) s[4 * i + e] = __float_as_uint(-INFINITY);
-                                if (key < lo1 || key >= hi1) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
+                                for (int e = 0; e < 2; ++e) {
+                                    const int key = 8 * i + 2 * ga + e;
+                                    if (key < lo0 || key >= hi0) s[4 * i + e] = __float_as_uint(-INFINITY);
+                                    if (key < lo1 || key >= hi1) s[4 * i + 2 + e] = __float_as_uint(-INFINITY);
+                                }
+                        } else {  // rows that see all of the tile and rows that see nothing of it
+                            const bool none0 = lo0 >= hi0, none1 = lo1 >= hi1;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                s[4 * i] = none0 ? __float_as_uint(-INFINITY) : s[4 * i];
+                                s[4 * i + 1] = none0 ? __float_as_uint(-INFINITY) : s[4 * i + 1];
+                                s[4 * i + 2] = none1 ? __float_as_uint(-INFINITY) : s[4 * i + 2];
+                                s[4 * i + 3] = none1 ? __float_as_uint(-INFINITY) : s[4 * i + 3];
                             }
+                        }
                     } else {
                         // in virtual keys a row sees v <= hi with v >= lo or v < ns; rows past the
                         // chunk (a ragged last item) as its last row: computed, never stored
@@ -1122,7 +1166,22 @@ int launch_rows(const PrefillArgs &a, const int32_t *key_ranges) {
                                : std::min<int64_t>(a.max_context_len, (int64_t)a.window + kBM / G + a.num_sinks);
     const int sms = device_sm_count();
     int cluster = 1;
-    while (cluster < 16 && items * cluster * 2 <= sms && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
+    if constexpr (CROSS) {
+        // A split item has no next one under its end, and pays about 8 us for that.  One sequence of 500,
+        // 1500 and 6000 keys, whole | in twos | fours | eights (us): 32 items 12, 23, 74 | 14, 19, 46 |
+        // 12, 15, 28 | 18, 20, 28; 72 items 12, 24, 73 | 15, 20, 45 | 15, 19, 35 | 32, 37, 53; 144 items
+        // 14, 25, 75 | 19, 27, 57 | 28, 36, 66; 16 items of 6000 keys 28 in fours, 25 in eights.
+        const int64_t slots = 2 * (int64_t)sms;
+        // listed items: a sequence's last one is half full on average
+        const int64_t likely = p.listed ? (a.num_tokens / (kBM / G) + (a.num_seqs + 1) / 2) * (int64_t)a.num_kv_heads : items;
+        if (likely * 4 <= sms ? keys > 384 : likely * 4 <= slots * 63 / 64 && keys > 1024) cluster = 4;
+        // Contexts of several sequences are ragged as a rule, which the host cannot see: 160 items of 100 to
+        // 3000 keys 46 us whole, 35 in twos, of 500 to 8000 keys 103 and 63; were all of 1500 keys, 33 and 44.
+        else if (likely * 2 <= slots ? keys > 2048 : a.num_seqs > 1 && likely <= slots * 4 / 5 && keys > 1024) cluster = 2;
+        while (cluster >= 4 && cluster < 16 && likely * cluster * 2 <= sms && keys > 512 * (int64_t)cluster) cluster *= 2;
+    } else {
+        while (cluster < 16 && items * cluster * 2 <= sms && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;
+    }
     const int64_t rows = (int64_t)a.num_blocks * a.block_size;
     if (rows <= 0 || rows > INT32_MAX || items > INT32_MAX) return PA_ERR_INVALID_ARG;
     // Q boxes are 64 elements (the swizzle span) wide and cover the G heads of one kv head for
