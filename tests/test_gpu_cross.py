@@ -358,3 +358,71 @@ def test_runs_are_alike(dtype, rows):
     a = cross(case, t=t)
     for _ in range(3):
         assert torch.equal(a, cross(case, t=t))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+def test_pools_past_32_bits_of_bytes(dtype, rows):
+    # the same blocks at the far end of a pool of more than 2^32 bytes
+    case = make_case(dtype, 8, 8, 128, 32, [300, 77], [rows, rows], "mixed", seed=3)
+    t = case.cuda()
+    far = (1 << 32) // (32 * 8 * 128 * case.key_cache.element_size()) + 50
+    for k in ("key_cache", "value_cache"):
+        big = torch.empty((far + case.key_cache.shape[0], *t[k].shape[1:]), dtype=dtype, device="cuda")
+        big[far:] = t[k]
+        t[k] = big
+    t["tables"] = torch.where(t["tables"] >= 0, t["tables"] + far, t["tables"])
+    out = cross(case, t=t)
+    torch.cuda.synchronize()
+    assert_close(out, case, FP32)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_tables_wider_than_the_contexts(rows):
+    # what stands behind a context's last block is never looked at
+    case = make_case(BF16, 8, 2, 64, 16, [300, 0, 41], [rows] * 3, seed=9, width=50)
+    used = (case.ctx[:, None] + 15) // 16
+    case.tables = torch.where(torch.arange(50)[None] < used, case.tables, torch.full_like(case.tables, 2 ** 31 - 1))
+    check(case)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_rows_blind_to_whole_tiles(dtype, shift):
+    # blocks of rows that see everything beside rows that see nothing, a key, the first half or the second
+    C, n = 640, 64
+    spans = [(0, C), (0, 0), (5, 6), (0, C // 2), (C // 2, C), (64, 128), (100, 101), (0, C)]
+    ranges = [spans[((r + shift) // 8) % len(spans)] for r in range(2 * n)]
+    check(make_case(dtype, 8, 2, 128, 16, [C, C], [n, n], ranges, seed=shift), dtype)
+    check(make_case(dtype, 4, 4, 64, 32, [C, C], [n, n], ranges, seed=shift), dtype)
+
+
+def test_the_largest_number_of_items_is_refused_not_cut():
+    import paged_kv_attention_write_gb300 as pa
+    t = make_case(BF16, 4, 2, 64, 16, [50], [1], seed=1, single=True).cuda()
+    for kw, code in ((dict(max_query=2 ** 31), -1), (dict(max_ctx=2 ** 40), -1), (dict(scale=0.0), -1), (dict(scale=float("inf")), -1)):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_cross_attention(torch.empty_like(t["query"]), t["query"], None, kw.get("max_query", 1), t["key_cache"],
+                                  t["value_cache"], t["tables"], t["ctx"], kw.get("max_ctx", 50), kw.get("scale", 1.0))
+        assert e.value.code == code
+
+
+def test_refusals():
+    import paged_kv_attention_write_gb300 as pa
+    case = make_case(BF16, 4, 2, 64, 16, [50, 20], [3, 2], "mixed", seed=1)
+    t = case.cuda()
+    ok = dict(out=torch.empty_like(t["query"]), query=t["query"], query_start_loc=t["starts"], max_query_len=3,
+              key_cache=t["key_cache"], value_cache=t["value_cache"], block_tables=t["tables"], context_lens=t["ctx"],
+              max_context_len=50, scale=1.0, key_ranges=t["ranges"])
+    pa.pa_cross_attention(**ok)
+    for over in (dict(key_ranges=t["ranges"].long()), dict(key_ranges=t["ranges"][:4]), dict(key_ranges=t["ranges"].t()),
+                 dict(key_ranges=t["ranges"].cpu()), dict(key_ranges=t["ranges"].flatten()), dict(query_start_loc=None),
+                 dict(query_start_loc=t["starts"][:2]), dict(query_start_loc=t["starts"].long()),
+                 dict(query=t["query"].transpose(0, 1)), dict(value_cache=t["value_cache"].float()),
+                 dict(context_lens=t["ctx"].cpu()), dict(block_tables=t["tables"].t()), dict(out=ok["out"][:2]),
+                 dict(status=torch.zeros(1, device="cuda")), dict(max_query_len=-1), dict(max_context_len=-1),
+                 dict(query=torch.empty((5, 4, 64 + 4), dtype=BF16, device="cuda")[:, :, 4:])):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_cross_attention(**{**ok, **over})
+        assert e.value.code == -1
+    torch.cuda.synchronize()

@@ -261,3 +261,73 @@ def test_captured_loop_grows_and_shrinks_in_place(S):
         free, cached, num_free = r["free"], r["context"], r["num_free"]
     assert t.tolist() == tables and c.tolist() == cached and nf.item() == num_free
     assert f.tolist()[:num_free] == free[:num_free] and status.item() == 0
+
+
+def test_tables_past_32_bits_of_entries():
+    # 60000 rows of 40000 entries: the last rows' entries lie past 2^31
+    import paged_kv_attention_write_gb300 as pa
+    S, width, bs = 60000, 40000, 8
+    t = torch.full((S, width), -1, dtype=I32, device="cuda")
+    cached = torch.zeros(S, dtype=I32, device="cuda")
+    new = (torch.arange(S, device="cuda") % 3 * 9).to(I32)
+    total = int(new.sum())
+    blocks = int(((new + 7) // 8).sum())
+    free = torch.randperm(blocks + 5, device="cuda").to(I32)
+    nf = torch.tensor([blocks + 5], dtype=I32, device="cuda")
+    ctx, st, pos = torch.zeros_like(cached), torch.zeros(S + 1, dtype=I32, device="cuda"), torch.zeros(total, dtype=I32, device="cuda")
+    slots, status = torch.zeros(total, dtype=torch.int64, device="cuda"), torch.zeros(1, dtype=I32, device="cuda")
+    pa.pa_tables_extend(t, ctx, st, pos, slots, nf, cached, new, free, nf, bs, blocks + 5, status=status)
+    want = ref.extend([[-1] * 3] * S, [0] * S, new.tolist(), free.tolist(), blocks + 5, total, bs, blocks + 5)
+    assert t[:, :3].tolist() == want["tables"] and slots.tolist() == want["slots"] and pos.tolist() == want["positions"]
+    assert status.item() == 0 and nf.item() == 5 and bool((t[:, 3:] == -1).all())
+    keep = torch.zeros_like(ctx)
+    pa.pa_tables_trim(free, ctx, nf, t, ctx, keep, nf, bs, blocks + 5, status=status)
+    assert nf.item() == blocks + 5 and sorted(free.tolist()) == list(range(blocks + 5)) and status.item() == 0
+
+
+@pytest.mark.parametrize("most", [3, 4, 5, 6])
+@pytest.mark.parametrize("S", [70, 2060])
+def test_a_few_tokens_each(S, most):
+    # at most four tokens: every thread sees to its own sequences; one with five: the shared-out path
+    rng, cached, tables, free, extra, NB = state(S + most, S, 60, 8, 2 * S, 10)
+    new = rng.integers(0, 4, S)
+    new[S // 2] = most
+    for T in (int(new.sum()) + 40, int(new.sum()), int(new.sum()) - 3):
+        check_extend(tables, cached, new, free, extra, T, 8, NB)
+    check_extend(tables, cached, new, free, extra // 9, int(new.sum()), 8, NB)
+    keep = np.maximum(0, cached - 8 * rng.integers(0, 4, S))
+    keep[S // 2] = max(0, cached[S // 2] - 8 * most)
+    check_trim(tables, cached, keep, free, extra, 8, NB)
+    check_trim(tables, cached, keep, free[:extra + S // 3], extra, 8, NB)
+
+
+def test_refusals():
+    import paged_kv_attention_write_gb300 as pa
+
+    def t(*shape, dtype=I32):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    ok = dict(block_tables=t(3, 2), context_lens=t(3), query_start_loc=t(4), positions=t(8), slot_mapping=t(8, dtype=torch.int64),
+              num_free_out=t(1), cached_lens=t(3), new_lens=t(3), free_blocks=t(9), num_free=t(1), block_size=16, num_blocks=20)
+    pa.pa_tables_extend(**ok)
+    for over in (dict(cached_lens=t(2)), dict(new_lens=t(3, dtype=torch.int64)), dict(block_tables=t(6)), dict(query_start_loc=t(3)),
+                 dict(positions=t(7)), dict(slot_mapping=t(8)), dict(num_free=t(0)), dict(block_tables=t(2, 3).t()),
+                 dict(context_lens=t(6)[::2]), dict(free_blocks=t(18)[::2]), dict(slot_mapping=t(16, dtype=torch.int64)[::2]),
+                 dict(num_free=t(1).cpu()), dict(query_start_loc=t(4).cpu()), dict(positions=t(8).float()),
+                 dict(status=t(1, dtype=torch.int64)), dict(block_tables=t(3, 2).cpu())):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_tables_extend(**{**ok, **over})
+        assert e.value.code == -1
+    for over, code in ((dict(block_size=12), -2), (dict(num_blocks=-1), -1), (dict(num_blocks=2 ** 31), -1)):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_tables_extend(**{**ok, **over})
+        assert e.value.code == code
+    trim = dict(free_blocks=t(9), context_lens=t(3), num_free_out=t(1), block_tables=t(3, 2), cached_lens=t(3), keep_lens=t(3),
+                num_free=t(1), block_size=16, num_blocks=20)
+    pa.pa_tables_trim(**trim)
+    for over in (dict(keep_lens=t(4)), dict(free_blocks=t(9, dtype=torch.int64)), dict(num_free_out=t(0)), dict(cached_lens=t(6)[::2]),
+                 dict(keep_lens=t(3).cpu())):
+        with pytest.raises(pa.PAError) as e:
+            pa.pa_tables_trim(**{**trim, **over})
+        assert e.value.code == -1
+    torch.cuda.synchronize()
