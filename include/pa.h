@@ -24,8 +24,7 @@
  *  - The return value is PA_OK (0) or a negative PA_ERR_* code.  Argument
  *    errors are detected on the host before anything is launched.  A failed
  *    launch returns PA_ERR_CUDA.
- *  - The first call of pa_decode, pa_decode_rope, pa_decode_noalloc or
- *    pa_prefill_chunk on a device raises its kernels' shared-memory limit
+ *  - The first call of an attention or pa_tables_* entry point on a device raises its kernels' shared-memory limit
  *    (cudaFuncSetAttribute) and may load the library's device code into the
  *    current context; make that first call outside stream capture.  Calls
  *    from several host threads are safe (per-device setup is atomic).
@@ -497,8 +496,12 @@ int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *args);
  *   out[r][h] = sum_j softmax_j(scale * q[r][h] . k_j) v_j over begin_r <= j < end_r;
  *   a row that sees no key is all zeros.  Rows of no sequence are left as they were.
  * F32, F16 and BF16 caches, any number of rows.  scale <= 0 returns PA_ERR_INVALID_ARG.  There
- * is no workspace; a call may be captured into a CUDA graph after one eager call with its types
- * and head dimension on the device.  Contexts below zero, past max_context_len or past the
+ * is no workspace; a call may be captured into a CUDA graph after one eager call with its cache
+ * type and head dimension on the device.  Few rows (up to eight
+ * (row, query head) columns per kv head, more where the call is small) and F32 caches keep their
+ * weights as pa_decode_window does; the others round them to the cache's type before the products
+ * and the row sums, as pa_prefill_window does.  Which of the two runs, and how a row's keys are
+ * split, depends on the call's sizes alone.  Contexts below zero, past max_context_len or past the
  * block table are reported and clamped.  A block-table entry is read only if a row's range
  * reaches its block; what the cache holds in slots that no row of the sequence sees is never used,
  * not even NaN.  Values that some row of a sequence sees must be finite (a key that one row
@@ -517,7 +520,9 @@ int pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, const i
  * the sequences' lengths, so that a step loop (captured into a CUDA graph, say) grows its own
  * sequences and sends nothing from the host.  The free blocks are a stack in device memory:
  * free_blocks int32 [free_capacity], of which the first *num_free are free.  These pools share no
- * blocks between sequences (pa_kv_manager.h does, on the host).  One launch each; results do not depend on timing.
+ * blocks between sequences (pa_kv_manager.h does, on the host).  Each call is one launch, keeps
+ * nothing between calls, and its results do not depend on timing.  At most 65535 sequences;
+ * block_size 8, 16 or 32.  The tensors of a call overlap only where it says so.
  *
  * pa_tables_extend -- sequence s grows from cached_lens[s] to cached_lens[s] + new_lens[s] tokens.
  *

@@ -92,9 +92,12 @@ int launch_cross_rows(const CrossArgs &c) {
 
 int launch_cross(const CrossArgs &c) {
     const PrefillArgs &a = c.a;
-    if (a.kv_dtype == PA_F32) return launch_cross_rows(c);
     // Every kernel that a call with this type and head dimension may take is loaded by the first one on
     // a device, so that any later one may be captured.
+    if (a.kv_dtype == PA_F32) {
+        const int rc = a.head_dim == 64 ? load_f32<64, true>() : load_f32<128, true>();
+        return rc == PA_OK ? launch_cross_rows(c) : rc;
+    }
     const bool half = a.kv_dtype == PA_F16, wide = a.head_dim == 128;
     int rc = half ? (wide ? load_16<F16, 128, true>() : load_16<F16, 64, true>())
                   : (wide ? load_16<BF16, 128, true>() : load_16<BF16, 64, true>());

@@ -49,6 +49,21 @@
 // stores (a timing-only build of the 507 us step) 469 us were left; with no K and V loads at
 // all, 427 of 500.
 //
+// Cross attention (CROSS): no order among the keys, each row sees [begin, end) of its own.  An item
+// walks the blocks from the first to the last key that one of its rows sees; blocks that none
+// reaches are not loaded, and only tiles that some row does not see whole are masked: a warp
+// whose rows see nothing of a tile stores zero weights and is done with it.  The ranges of an item's
+// rows wait in shared memory beside its slot.  Sequences with long contexts go first, and where
+// ranges are given the last rows of all sequences, which see most of what stands before them.
+// Measured (us): fp16, 8 x 512 rows of 64 q / 8 kv heads over 4096 to 12288 keys, D 128: 842 (1.32
+// PFLOP/s; 904 in the sequences' order); bf16, 4 x 512 rows of 32 / 8 heads beside four images of 1601
+// keys: 94 (its longest items, 101 tiles, take 90); 23 ragged chunks of 8 / 1 heads beside three
+// images: 32 in clusters of two, 48 whole.  Half of each item's rows blind to all tiles but the
+// first: 290 with scores masked one by one, 225 so, 187 when all rows see all.  A CTA per SM with the
+// warps, rings and TMEM of two, both halves on one item, was tried for items of unequal length: the
+// ragged chunks 33, 336 items of 500 to 8000 keys 134 -> 94, but the images 94 -> 96, 256 items of
+// 6000 keys 92 -> 98 and the wide case 842 -> 912: nothing runs under an item's beginning and end.
+//
 // Warps: 0 items, TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the
 // rows of V that no row of the item looks at, so that stale or NaN slots never meet a zero
 // weight), 4-11 softmax and output, each a 16-row slab through the 16-lane TMEM shapes.
@@ -789,7 +804,7 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 tc_fence_after();
                 const uint32_t tS = tL + sb * kBN;
                 // the tile is for other rows of the item (half of the rows of every item blind to all tiles but the
-                // first: 290 us with their scores masked one by one, 187 where all rows see all)
+                // first: 290 us with their scores masked one by one, 225 so, 187 where all rows see all)
                 if (CROSS && blind) {
                     uint32_t w[16];
 #pragma unroll

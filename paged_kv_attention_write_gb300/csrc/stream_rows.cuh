@@ -45,7 +45,16 @@
 // nothing ran under their beginnings and ends.
 // Cross attention (CROSS): the eight columns are tokens times query heads of the kv head, the keys
 // are those from the first to the last that one of the item's tokens sees, blocks that none
-// reaches are not loaded, and a score is masked by its own token's range.
+// reaches are not loaded, and a score is masked by its own token's range.  Contexts are as long as
+// they come, so where a second wave of CTAs would be uneven the longest go first.
+// Measured (us, calls in a row): bf16, 64 sequences of one row over 1600 to 6404 keys, 32 q / 8 kv heads,
+// D 128: 154 (6.89 TB/s; 194 in the sequences' order); fp16, 16 sequences of five rows over 400 to
+// 1500 keys, 16 / 16 heads, D 64: 18.5 (3.5 TB/s: 256 items, so that 104 of the SMs have two and 48
+// one); one row over 1500 keys 6.4 (launch and the chain named above); fp32, 19 sequences of 1 to 3
+// rows over up to 1333 keys, 16 / 4 heads: 17.1.  Tried for D 64: CTAs of eight consumer warps (18.9 ->
+// 19.4), and four CTAs per SM on rings of half the size: 512 items of 1000 keys 34 -> 25 us, 1024 of
+// 4000 keys 180 -> 163, but 512 of 1000 to 4000 keys of one query head each 57 -> 66, 2048 of 4000
+// keys 316 -> 326, 32 of 100 to 8000 keys 14.1 -> 17.7; no rule on the sizes told them apart.
 // Every mbarrier wait is bounded in time; if one gives up, the boxes under way still land before the
 // CTA leaves (not run on a GPU: it would take a wait of two seconds).
 #pragma once
@@ -1039,6 +1048,21 @@ int launch_16(const Params &p, int cluster, dim3 grid, int64_t pairs, int warps,
                                Shape<T, D>::SMEM, cluster, st, km, vm, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+// The same for the kernels of fp32 caches, one per number of columns.
+template <int D, bool CROSS>
+int load_f32() {
+    static std::atomic<int> loaded[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices && loaded[dev].load(std::memory_order_acquire)) return PA_OK;
+    for (auto kernel : {stream_rows_kernel<F32, D, 1, CROSS>, stream_rows_kernel<F32, D, 2, CROSS>,
+                        stream_rows_kernel<F32, D, 4, CROSS>, stream_rows_kernel<F32, D, 8, CROSS>})
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<F32, D>::SMEM) != cudaSuccess)
+            return PA_ERR_CUDA;
+    if (dev >= 0 && dev < kMaxDevices) loaded[dev].store(1, std::memory_order_release);
+    return PA_OK;
 }
 
 template <int D, bool CROSS>
