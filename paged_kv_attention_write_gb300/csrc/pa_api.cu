@@ -402,7 +402,7 @@ int pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, const i
                              num_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
                              kv_dtype);
     if (rc != PA_OK) return rc;
-    if (num_tokens < 0 || max_query_len < 0 || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
+    if (num_tokens < 0 || (query_start_loc && max_query_len < 0) || !(scale > 0.f)) return PA_ERR_INVALID_ARG;
     if (!query_start_loc && num_tokens != num_seqs) return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || nothing) return PA_OK;
     if (!aligned(query_start_loc, 4) || !aligned(key_ranges, 8) || !aligned(status, 4)) return PA_ERR_INVALID_ARG;
