@@ -92,7 +92,7 @@ struct Params {
     int by_length;           // sequences with long contexts first
 };
 
-template <class T, int D>
+template <class T, int D, bool CROSS>
 struct Shape {
     static constexpr bool kF32 = std::is_same<T, F32>::value;
     static constexpr int GROUP_BYTES = 8 * D * T::kBytes;        // 8 tokens of one kv head
@@ -100,7 +100,8 @@ struct Shape {
     static constexpr int KV_BYTES = NGRP * GROUP_BYTES;
     static constexpr int NSTAGE = 3;
     static constexpr int NW = 4;                     // consumer warps
-    static constexpr int THREADS = (NW + 1) * 32;
+    static constexpr int NP = CROSS ? 2 : 1;         // producer warps: K and V together, or each its own
+    static constexpr int THREADS = (NW + NP) * 32;
     static constexpr int HW = kF32 ? 4 : 8;                      // query heads a warp holds
     static constexpr int PITCH = D + 4;                          // floats between the merge buffer's head rows
     static constexpr int OFF_O = NSTAGE * 2 * KV_BYTES;          // the CTA's merged output [8][D], then m, l [8]
@@ -314,7 +315,7 @@ __device__ __forceinline__ void store_pair(void *out, pa_dtype dt, int64_t idx, 
 
 template <class T, int D, bool CROSS>
 struct Consumer16 {
-    using Sh = Shape<T, D>;
+    using Sh = Shape<T, D, CROSS>;
     using Keys = KeysOf<CROSS>;
     uint32_t q[D / 16][2];  // Q^T as the 16 x 8 operand: head lane/4
     float o[D / 16][4];     // O^T: dims 16m + lane/4 (+8), heads 2(lane%4), +1
@@ -490,7 +491,7 @@ struct Consumer16 {
 // this takes 7 and 1).
 template <int D, int G, bool CROSS>
 struct Consumer32 {
-    using Sh = Shape<F32, D>;
+    using Sh = Shape<F32, D, CROSS>;
     using Keys = KeysOf<CROSS>;
     static constexpr int HW = G < 4 ? G : 4;     // query heads of this warp
     static constexpr int QS = G / HW;            // warps that share a key, on different heads
@@ -670,10 +671,10 @@ __device__ __forceinline__ bool output_at(const Params &p, const KeysOf<CROSS> &
 // items).  G is the number of columns (the group size, CROSS: times the tokens) for fp32 caches; 0
 // (1, 2, 4 or 8 of them) for 16-bit ones.
 template <class T, int D, int G, bool CROSS>
-__global__ void __launch_bounds__(Shape<T, D>::THREADS, 2)
+__global__ void __launch_bounds__(Shape<T, D, CROSS>::THREADS, 2)
 stream_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                      const Params p) {
-    using Sh = Shape<T, D>;
+    using Sh = Shape<T, D, CROSS>;
     constexpr int NGRP = Sh::NGRP, NSTAGE = Sh::NSTAGE, KVB = Sh::KV_BYTES, NW = Sh::NW, HW = Sh::HW;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>(
@@ -689,7 +690,7 @@ stream_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < NSTAGE; ++i) {
-            mbar_init(full0 + 8 * i, 1);
+            mbar_init(full0 + 8 * i, Sh::NP);
             mbar_init(empty0 + 8 * i, NW);
         }
         fence_barrier_init();
@@ -726,13 +727,13 @@ stream_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int stages = (v1 - v0 + NGRP - 1) / NGRP;
     volatile int *abort_v = abort_flag;
 
-    if (warp == NW) {
+    if (warp >= NW) {
         // ============================================================ producer
         const int per_block = p.block_size / 8;
         const int32_t *bt = p.block_tables + (int64_t)s * p.max_blocks_per_seq;
         const int per_stage = NGRP / unit;  // boxes of K, and of V
-        const bool is_v = lane >= per_stage, mine = lane < 2 * per_stage;
-        const int slot = (is_v ? lane - per_stage : lane) * unit;  // first group of the stage
+        const bool is_v = Sh::NP == 2 ? warp > NW : lane >= per_stage, mine = lane < (3 - Sh::NP) * per_stage;
+        const int slot = (Sh::NP == 1 && is_v ? lane - per_stage : lane) * unit;  // first group of the stage
         const uint32_t box_bytes = Sh::GROUP_BYTES * unit;
         const uint64_t policy = policy_evict_first();
         auto group_of = [&](int i) { return keys.logical(v0 + i * NGRP + slot); };
@@ -759,7 +760,7 @@ stream_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const unsigned boxes = __ballot_sync(kFullMask, valid);
             const uint32_t groups = __reduce_or_sync(kFullMask, valid && !is_v ? ((1u << unit) - 1u) << slot : 0u);
             if (lane == 0) {
-                loaded[st] = groups;
+                if (Sh::NP == 1 || !is_v) loaded[st] = groups;
                 mbar_arrive_expect_tx(full0 + 8 * st, __popc(boxes) * box_bytes);
             }
             __syncwarp();
@@ -889,7 +890,7 @@ template <class T, int D, bool CROSS>
 __global__ void __launch_bounds__(32)
 stream_rows_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const Params p, int depth) {
-    using Sh = Shape<T, D>;
+    using Sh = Shape<T, D, CROSS>;
     constexpr int GB = Sh::GROUP_BYTES, STEP = 4 * GB;
     static_assert(Sh::HW * (Sh::PITCH + 2) * 4 <= STEP, "the result fits one step");
     extern __shared__ unsigned char smem_raw[];
@@ -998,7 +999,7 @@ stream_rows_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
 
 template <class T, int D, int G, bool CROSS>
 int launch_typed(const Params &p, int cluster, dim3 grid, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
-    using Sh = Shape<T, D>;
+    using Sh = Shape<T, D, CROSS>;
     static std::atomic<int> smem_ready[kMaxDevices];  // per device: shared-memory limit raised
     return launch_pdl_cluster(stream_rows_kernel<T, D, G, CROSS>, smem_ready, grid, dim3(Sh::THREADS), Sh::SMEM, cluster, st,
                               km, vm, p) == cudaSuccess
@@ -1009,7 +1010,7 @@ int launch_typed(const Params &p, int cluster, dim3 grid, const CUtensorMap &km,
 // A 16-bit cache's steps of a ring of the warps' kernel, at most, and the rest of its shared memory.
 constexpr int kMostSteps = 16, kWarpRest = 1024 + 8 * kMostSteps;
 template <class T, int D>
-constexpr int kStepBytes = 4 * Shape<T, D>::GROUP_BYTES;
+constexpr int kStepBytes = 4 * Shape<T, D, false>::GROUP_BYTES;
 
 // A device's first call loads both kernels of 16-bit caches, with the shared memory that any call
 // asks for: a later one may be captured, whichever kernel it takes.
@@ -1020,7 +1021,7 @@ int load_16() {
     if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices && loaded[dev].load(std::memory_order_acquire)) return PA_OK;
     if (cudaFuncSetAttribute(stream_rows_kernel<T, D, 0, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Shape<T, D>::SMEM) != cudaSuccess ||
+                             Shape<T, D, CROSS>::SMEM) != cudaSuccess ||
         cudaFuncSetAttribute(stream_rows_warp_kernel<T, D, CROSS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMostSteps * kStepBytes<T, D> + kWarpRest) != cudaSuccess)
         return PA_ERR_CUDA;
@@ -1044,8 +1045,8 @@ int launch_16(const Params &p, int cluster, dim3 grid, int64_t pairs, int warps,
         e = launch_pdl_cluster(stream_rows_warp_kernel<T, D, CROSS>, warps_ready, dim3((unsigned)pairs), dim3(32),
                                depth * STEP + kWarpRest, 1, st, km, vm, p, depth);
     } else {
-        e = launch_pdl_cluster(stream_rows_kernel<T, D, 0, CROSS>, clusters_ready, grid, dim3(Shape<T, D>::THREADS),
-                               Shape<T, D>::SMEM, cluster, st, km, vm, p);
+        e = launch_pdl_cluster(stream_rows_kernel<T, D, 0, CROSS>, clusters_ready, grid, dim3(Shape<T, D, CROSS>::THREADS),
+                               Shape<T, D, CROSS>::SMEM, cluster, st, km, vm, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1059,7 +1060,7 @@ int load_f32() {
     if (dev >= 0 && dev < kMaxDevices && loaded[dev].load(std::memory_order_acquire)) return PA_OK;
     for (auto kernel : {stream_rows_kernel<F32, D, 1, CROSS>, stream_rows_kernel<F32, D, 2, CROSS>,
                         stream_rows_kernel<F32, D, 4, CROSS>, stream_rows_kernel<F32, D, 8, CROSS>})
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<F32, D>::SMEM) != cudaSuccess)
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<F32, D, CROSS>::SMEM) != cudaSuccess)
             return PA_ERR_CUDA;
     if (dev >= 0 && dev < kMaxDevices) loaded[dev].store(1, std::memory_order_release);
     return PA_OK;
