@@ -38,9 +38,10 @@ int launch_cross_rows(const CrossArgs &c) {
     p.token_groups = (longest - 1) / p.tokens + 1;
     const int columns = p.tokens * p.group;
     // Clusters as in decode_window.cu: the CTAs of one full wave, none with less than one stage of
-    // keys (two past eight CTAs).  A ninth more than a wave still pays in twos where the contexts are
-    // ragged, which the host cannot see, and costs little where they are not (164 items of up to 1333
-    // fp32 keys 26.4 us whole, 17.5 in twos).
+    // keys (two past eight CTAs).  In twos a ninth more than a wave pays where the contexts are ragged
+    // (164 items of up to 1333 fp32 keys 26.4 us whole, 17.5 in twos; 160 of 400 to 4000 bf16 keys 52 and
+    // 36) and costs where they are not (160 items of 4000 keys 56 and 75).  The host cannot see that;
+    // it takes ragged numbers of rows as the sign of it.
     const int sms = std::max(1, device_sm_count());
     const int64_t slots = 2 * sms, most = a.max_context_len;
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
@@ -48,7 +49,7 @@ int launch_cross_rows(const CrossArgs &c) {
     // those that have rows: of ragged sequences some items are empty and gone at once
     const int64_t live = std::min<int64_t>(items, (p.tokens == 1 ? a.num_tokens : a.num_tokens / p.tokens + (int64_t)a.num_seqs) *
                                                       a.num_kv_heads);
-    auto fit = [&](int size) { return slots * (size == 2 ? 71 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
+    auto fit = [&](int size) { return slots * (size == 2 ? (live < items ? 71 : 64) : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
     int cluster = 1;
     while (cluster < 16 && live * cluster * 2 <= fit(cluster * 2) &&
            most > stage_keys * cluster * (cluster < 8 ? 1 : 2))

@@ -1190,9 +1190,10 @@ int launch_rows(const PrefillArgs &a, const int32_t *key_ranges) {
         // listed items: a sequence's last one is half full on average
         const int64_t likely = p.listed ? (a.num_tokens / (kBM / G) + (a.num_seqs + 1) / 2) * (int64_t)a.num_kv_heads : items;
         if (likely * 4 <= sms ? keys > 384 : likely * 4 <= slots * 63 / 64 && keys > 1024) cluster = 4;
-        // Contexts of several sequences are ragged as a rule, which the host cannot see: 160 items of 100 to
-        // 3000 keys 46 us whole, 35 in twos, of 500 to 8000 keys 103 and 63; were all of 1500 keys, 33 and 44.
-        else if (likely * 2 <= slots ? keys > 2048 : a.num_seqs > 1 && likely <= slots * 4 / 5 && keys > 1024) cluster = 2;
+        // Ragged contexts gain beyond that: 160 items of 100 to 3000 keys 46 us whole, 35 in twos, of 500 to
+        // 8000 keys 103 and 63; were all of 1500 keys, 33 and 44.  The host cannot see them; it takes ragged
+        // chunks as the sign of them.
+        else if (likely * 2 <= slots ? keys > 2048 : p.listed && likely <= slots * 4 / 5 && keys > 1024) cluster = 2;
         while (cluster >= 4 && cluster < 16 && likely * cluster * 2 <= sms && keys > 512 * (int64_t)cluster) cluster *= 2;
     } else {
         while (cluster < 16 && items * cluster * 2 <= sms && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;

@@ -46,13 +46,16 @@
 // Cross attention (CROSS): the eight columns are tokens times query heads of the kv head, the keys
 // are those from the first to the last that one of the item's tokens sees, blocks that none
 // reaches are not loaded, and a score is masked by its own token's range.  Contexts are as long as
-// they come, so where a second wave of CTAs would be uneven the longest go first.
+// they come, so where a second wave of CTAs would be uneven the longest go first, and a CTA that
+// has its SM for itself is bound by the issue of its boxes, so keys and values have a producer warp
+// each (one row of a kv head of D 64 over 4000 keys in one CTA 36 -> 30 us).
 // Measured (us, calls in a row): bf16, 64 sequences of one row over 1600 to 6404 keys, 32 q / 8 kv heads,
-// D 128: 154 (6.89 TB/s; 194 in the sequences' order); fp16, 16 sequences of five rows over 400 to
-// 1500 keys, 16 / 16 heads, D 64: 18.5 (3.5 TB/s: 256 items, so that 104 of the SMs have two and 48
-// one); one row over 1500 keys 6.4 (launch and the chain named above); fp32, 19 sequences of 1 to 3
-// rows over up to 1333 keys, 16 / 4 heads: 17.1.  Tried for D 64: CTAs of eight consumer warps (18.9 ->
-// 19.4), and four CTAs per SM on rings of half the size: 512 items of 1000 keys 34 -> 25 us, 1024 of
+// D 128: 152 (7.0 TB/s; 194 in the sequences' order); fp16, 16 sequences of five rows over 400 to
+// 1500 keys, 16 / 16 heads, D 64: 17.2 (3.8 TB/s: an SM takes in 50 to 53 GB/s at most, and 104 of
+// them have two of the 256 items); one row over 1500 keys 6.3 (launch and the chain named above); fp32,
+// 19 sequences of 1 to 3 rows over up to 1333 keys, 16 / 4 heads: 15.6.  Tried: rings of six stages
+// where an SM has one CTA (no change); for D 64, CTAs of eight consumer warps (17.9 -> 18.1), long and
+// short items on one SM (17.9 -> 18.4, the ranking), and with one producer warp four CTAs per SM on rings of half the size: 512 items of 1000 keys 34 -> 25 us, 1024 of
 // 4000 keys 180 -> 163, but 512 of 1000 to 4000 keys of one query head each 57 -> 66, 2048 of 4000
 // keys 316 -> 326, 32 of 100 to 8000 keys 14.1 -> 17.7; no rule on the sizes told them apart.
 // Every mbarrier wait is bounded in time; if one gives up, the boxes under way still land before the
