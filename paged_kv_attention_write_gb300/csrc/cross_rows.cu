@@ -56,7 +56,10 @@ int launch_cross_rows(const CrossArgs &c) {
         cluster *= 2;
     p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
     const int per_sm = (int)std::min<int64_t>(8, (live + sms - 1) / sms);
-    const bool by_warp = a.kv_dtype != PA_F32 && live > slots && most <= (per_sm * a.head_dim >= 320 ? 1152 : 384);
+    // A warp per item where many have few keys: 320 items of 100, 250 and 500 keys (D 128) 9.7, 16 and 27 us,
+    // clusters 12, 17 and 25; 800 items 13, 22 and 38, clusters 21, 29 and 42, of 1000 keys 70 and 71 (of 100
+    // to 1000 keys 55 and 46: a warp waits for the longest); D 64 alike.
+    const bool by_warp = a.kv_dtype != PA_F32 && live > slots && most <= (per_sm >= 5 ? 768 : 384);
     const int warps = by_warp ? per_sm : 0;
     // Long contexts first where a second wave of CTAs would otherwise end with one: 512 items of 1600
     // to 6404 keys 194 -> 155 us, 800 of 500 to 2500 108 -> 97; past four waves the lengths even out

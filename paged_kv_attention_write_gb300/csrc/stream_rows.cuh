@@ -155,13 +155,15 @@ struct CrossKeys {
         return cut.x < cut.y ? cut : make_int2(0, 0);
     }
     // The item of a number (sequence, tokens, kv head), for every thread; false when it has no rows.
-    // The ranges are left in `shared`, which the CTA must then meet on.
+    // The ranges are left in `shared`, which the CTA must then meet on.  RANKED: the CTA has a thread for
+    // each of kMostRanked sequences, so that by_length can be served.
+    template <bool RANKED>
     __device__ __forceinline__ bool find(const Params &p, unsigned number, int unit, int2 *shared, bool rep) {
         g = (int)(number % (unsigned)p.num_kv_heads);
         const unsigned rest = number / (unsigned)p.num_kv_heads;
         const int part = (int)(rest % (unsigned)p.token_groups), first = part * p.tokens;
         s = (int)(rest / (unsigned)p.token_groups);
-        if (p.by_length) {  // the sequence of rank s (a thread each)
+        if (RANKED && p.by_length) {  // the sequence of rank s (a thread each)
             // length and number in one key, so that a comparison ranks two sequences (lengths from 2^22
             // on count as alike: the order is only a matter of time)
             __shared__ __align__(16) int order[kMostRanked];
@@ -709,7 +711,8 @@ stream_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     __shared__ int2 row_ranges[8];
     KeysOf<CROSS> keys;
     if constexpr (CROSS) {
-        if (!keys.find(p, blockIdx.x / (unsigned)CS, unit, row_ranges, threadIdx.x == 0 && rank == 0)) return;
+        static_assert(Sh::THREADS >= kMostRanked, "a thread per ranked sequence");
+        if (!keys.template find<true>(p, blockIdx.x / (unsigned)CS, unit, row_ranges, threadIdx.x == 0 && rank == 0)) return;
         __syncthreads();
     } else {
         const int cap = min(p.max_blocks_per_seq * p.block_size, p.max_context_len);
@@ -916,7 +919,7 @@ stream_rows_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     __shared__ int2 row_ranges[8];
     KeysOf<CROSS> keys;
     if constexpr (CROSS) {
-        if (!keys.find(p, blockIdx.x, unit, row_ranges, lane == 0)) return;
+        if (!keys.template find<false>(p, blockIdx.x, unit, row_ranges, lane == 0)) return;
         __syncwarp();
         g = keys.g;
         s = keys.s;
