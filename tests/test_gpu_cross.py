@@ -426,3 +426,26 @@ def test_refusals():
             pa.pa_cross_attention(**{**ok, **over})
         assert e.value.code == -1
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=NAMES.get)
+@pytest.mark.parametrize("S", [153, 159, 160, 161, 200])
+def test_long_contexts_first_up_to_its_limit(dtype, S):
+    # more items than fit at once, of contexts that are equal, empty, and one much longer than the others
+    rng = np.random.default_rng(S)
+    ctx = [int(c) for c in rng.integers(380, 400, S)]
+    ctx[3], ctx[S // 2], ctx[-1] = 0, 1000, 1
+    check(make_case(dtype, 2, 2, 64, 16, ctx, [1] * S, seed=S, single=True))
+    check(make_case(dtype, 2, 2, 64, 16, ctx, [1] * S, "mixed", seed=S))
+
+
+@pytest.mark.parametrize("S", [2, 255, 256, 257, 300])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("ranges", [None, "mixed"])
+def test_chunks_of_long_contexts_first_up_to_their_limit(S, ragged, ranges):
+    rng = np.random.default_rng(S)
+    ctx = [int(c) for c in rng.integers(0, 150, S)]
+    ctx[S // 2] = 300
+    rows = [int(r) for r in rng.integers(0, 40, S)] if ragged else [11] * S
+    rows[-1] = 40 if ragged else 11
+    check(make_case(BF16, 8, 2, 64, 8, ctx, rows, ranges, seed=S))
