@@ -184,10 +184,13 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), std::atomic<int> *ready, d
     }
 }
 
-// launch_pdl_smem of a grid of clusters of `cluster` CTAs along x.
+// launch_pdl_smem of a grid of clusters of `cluster` CTAs along x, for a kernel whose calls ask for
+// shared memory of different sizes: the limit is raised to `limit`, the largest of them.  Were it set to
+// a call's own size, the first call that asks for more would be refused once, and a refused launch
+// invalidates the graph that its stream is capturing.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), std::atomic<int> *ready, dim3 grid, dim3 block, size_t smem,
-                               int cluster, cudaStream_t stream, const Args &...args) {
+                               size_t limit, int cluster, cudaStream_t stream, const Args &...args) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -195,7 +198,7 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), std::atomic<int> *ready
     for (int attempt = 0;; ++attempt) {
         const bool was_set = flag && flag->load(std::memory_order_acquire);
         if (!was_set) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)limit);
             // clusters of 16 CTAs are past the size that every device has to offer
             if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;

@@ -1133,7 +1133,7 @@ int launch_typed(const Params &p, int64_t items, int cluster, const CUtensorMap 
     if (rc != PA_OK) return rc;
     const dim3 grid((unsigned)(items * cluster)), block(kThreads);
     const cudaError_t e = cluster > 1 ? launch_pdl_cluster(prefill_rows_kernel<T, D, true, CROSS>, split_ready, grid, block,
-                                                           SMEM, cluster, st, qm, km, vm, p)
+                                                           SMEM, SMEM, cluster, st, qm, km, vm, p)
                                       : launch_pdl_smem(prefill_rows_kernel<T, D, false, CROSS>, whole_ready, grid, block,
                                                         SMEM, st, qm, km, vm, p);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

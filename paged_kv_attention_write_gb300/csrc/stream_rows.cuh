@@ -1007,8 +1007,8 @@ template <class T, int D, int G, bool CROSS>
 int launch_typed(const Params &p, int cluster, dim3 grid, const CUtensorMap &km, const CUtensorMap &vm, cudaStream_t st) {
     using Sh = Shape<T, D, CROSS>;
     static std::atomic<int> smem_ready[kMaxDevices];  // per device: shared-memory limit raised
-    return launch_pdl_cluster(stream_rows_kernel<T, D, G, CROSS>, smem_ready, grid, dim3(Sh::THREADS), Sh::SMEM, cluster, st,
-                              km, vm, p) == cudaSuccess
+    return launch_pdl_cluster(stream_rows_kernel<T, D, G, CROSS>, smem_ready, grid, dim3(Sh::THREADS), Sh::SMEM, Sh::SMEM,
+                              cluster, st, km, vm, p) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
 }
@@ -1049,10 +1049,10 @@ int launch_16(const Params &p, int cluster, dim3 grid, int64_t pairs, int warps,
     if (warps > 0) {
         const int depth = std::min(kMostSteps, (228 * 1024 / warps - 1024 - kWarpRest) / STEP);  // 1 KB per CTA is the system's
         e = launch_pdl_cluster(stream_rows_warp_kernel<T, D, CROSS>, warps_ready, dim3((unsigned)pairs), dim3(32),
-                               depth * STEP + kWarpRest, 1, st, km, vm, p, depth);
+                               depth * STEP + kWarpRest, kMostSteps * STEP + kWarpRest, 1, st, km, vm, p, depth);
     } else {
         e = launch_pdl_cluster(stream_rows_kernel<T, D, 0, CROSS>, clusters_ready, grid, dim3(Shape<T, D, CROSS>::THREADS),
-                               Shape<T, D, CROSS>::SMEM, cluster, st, km, vm, p);
+                               Shape<T, D, CROSS>::SMEM, Shape<T, D, CROSS>::SMEM, cluster, st, km, vm, p);
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -351,7 +351,7 @@ int launch(const TablesArgs &a, int64_t work) {
     int cluster = 1;
     while (cluster < 16 && work > (int64_t)kThreads * cluster) cluster *= 2;
     const int log2 = a.block_size == 8 ? 3 : a.block_size == 16 ? 4 : 5;
-    return launch_pdl_cluster(tables_kernel<EXTEND>, ready, dim3(cluster), dim3(kThreads), 0, cluster, a.stream, a, log2) ==
+    return launch_pdl_cluster(tables_kernel<EXTEND>, ready, dim3(cluster), dim3(kThreads), 0, 0, cluster, a.stream, a, log2) ==
                    cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
