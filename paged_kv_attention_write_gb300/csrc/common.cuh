@@ -180,6 +180,7 @@ cudaError_t launch_pdl_smem(void (*kernel)(KArgs...), std::atomic<int> *ready, d
         }
         e = launch_pdl(kernel, grid, block, smem, stream, args...);
         if (e == cudaSuccess || !was_set || attempt > 0) return e;
+        cudaGetLastError();  // the second launch's success would come back as this one's error
         flag->store(0, std::memory_order_release);
     }
 }
@@ -221,6 +222,7 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), std::atomic<int> *ready
         e = cudaLaunchKernelEx(&cfg, kernel, args...);
         if (e == cudaSuccess) e = cudaGetLastError();
         if (e == cudaSuccess || !was_set || attempt > 0) return e;
+        cudaGetLastError();  // as in launch_pdl_smem
         flag->store(0, std::memory_order_release);
     }
 }
