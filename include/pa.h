@@ -30,10 +30,13 @@
  *    from several host threads are safe (per-device setup is atomic).
  *  - Values that only the device can see (slot numbers, block ids, context
  *    lengths) are range-checked inside the kernels: an out-of-range value is
- *    never dereferenced; the offending token / block is skipped and, if
- *    `status` is not NULL, the matching PA_DEVERR_* bit is OR-ed into the
- *    device int32 `*status`.  The caller clears *status and reads it after
- *    synchronising.
+ *    never dereferenced and, if `status` is not NULL, the matching PA_DEVERR_*
+ *    bit is OR-ed into the device int32 `*status`.  The offending token / copy
+ *    pair is skipped.  The keys of an offending block are left out of the
+ *    softmax by pa_decode_window, by pa_cross_attention for F32 caches and
+ *    where it keeps its weights as pa_decode_window does; elsewhere they and
+ *    their values count as zeros.  The caller clears *status and reads it
+ *    after synchronising.
  *
  * Layouts (S sequences, Hq query heads, Hkv kv heads, D head dim, bs block
  * size, NB blocks in the pool; G = Hq / Hkv; query head h reads kv head h / G)

@@ -387,14 +387,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constan
                     break;
                 }
                 const bool in_range = lane < nb && j * kBN + lane * bs < it.kv_end;
-                const bool valid = in_range && my_id >= 0 && my_id < p.num_blocks;
+                const bool valid = my_id >= 0 && my_id < p.num_blocks;
                 if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
-                const unsigned mine = __ballot_sync(kFullMask, valid);
+                const unsigned mine = __ballot_sync(kFullMask, in_range);
                 if (lane == 0) mbar_expect_tx(full, __popc(mine) * box_bytes);
                 __syncwarp();
-                if (valid) {
+                if (in_range) {  // a box past the pool's end is filled with zeros: a bad id's keys and values
                     const uint32_t dst = ring + st * Sh::KV_BYTES + lane * box_bytes;
-                    tma_load_5d(dst, map, 0, 0, 0, my_id * (bs / 8), it.g, full, policy);
+                    tma_load_5d(dst, map, 0, 0, 0, (valid ? my_id : p.num_blocks) * (bs / 8), it.g, full, policy);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full);

@@ -658,9 +658,9 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 id0 = id1;
                 id1 = block_id(t + 2);
                 const bool in_range = CROSS ? id != INT32_MIN : lane < nb && (j0 + t) * nb + lane < it.blocks;
-                const bool valid = in_range && id >= 0 && id < p.num_blocks;
+                const bool valid = id >= 0 && id < p.num_blocks;
                 if (in_range && !valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
-                const uint32_t bytes = __popc(__ballot_sync(kFullMask, valid)) * box_bytes;
+                const uint32_t bytes = __popc(__ballot_sync(kFullMask, in_range)) * box_bytes;
                 const int st = (done + t) % NS;
                 int w_ok = 1;
                 if (lane == 0) {
@@ -669,9 +669,12 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
                 }
                 ok = __shfl_sync(kFullMask, w_ok, 0);
                 if (!ok) break;
-                if (valid)
-                    tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0, id << (bl - 3), it.g,
-                                bar(full + st), policy);
+                // A box past the pool's end is filled with zeros: a bad id's keys and values (not what the ring
+                // held, another sequence's or NaN).  Masking such keys in the softmax instead took 3 to 8 % of
+                // every call.
+                if (in_range)
+                    tma_load_5d(ring + st * Sh::KV_BYTES + lane * box_bytes, map, 0, 0, 0,
+                                (valid ? id : p.num_blocks) << (bl - 3), it.g, bar(full + st), policy);
                 __syncwarp();
                 if (!SPLIT && is_k && t == n - 1) ask();
             }
