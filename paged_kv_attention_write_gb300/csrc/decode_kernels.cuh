@@ -543,11 +543,10 @@ decode_split_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
                 const int tb = t0 + b * rows;
                 if (tb >= ctx) break;
                 const int id = bt[tb / bs];
-                if (id < 0 || id >= p.num_blocks) {  // never dereferenced; the stage keeps stale data
-                    report(p.status, PA_DEVERR_BLOCK_ID);
-                    continue;
-                }
-                const int row = id * bs + tb % bs;
+                const bool valid = id >= 0 && id < p.num_blocks;
+                if (!valid) report(p.status, PA_DEVERR_BLOCK_ID);  // never dereferenced
+                // a box past the pool's end is filled with zeros: a bad id's keys and values
+                const int row = valid ? id * bs + tb % bs : p.num_blocks * bs;
                 mbar_expect_tx(full, 2 * box_bytes);
                 tma_load_3d(kdst + b * box_bytes, &kmap, 0, hg * HG, row, full, policy);
                 tma_load_3d(kdst + KVB + b * box_bytes, &vmap, 0, hg * HG, row, full, policy);

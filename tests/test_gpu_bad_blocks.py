@@ -132,10 +132,13 @@ def test_one_long_context(dtype, rows):
 @pytest.mark.parametrize("D,bs", [(64, 8), (64, 32), (128, 16)])
 @pytest.mark.parametrize("Hkv,G,S", [(8, 1, 6), (2, 4, 6), (8, 8, 12), (8, 1, 120)])
 def test_single_tokens(dtype, D, bs, Hkv, G, S):
-    # 120 sequences of 8 heads: a warp per item
+    # 12 sequences of 8 x 8 heads: the decode's tensor-core rows; 120 of 8 heads: a warp per item
     import paged_kv_attention_write_gb300 as pa
     ctx = [(CTX[i % 6] + 5 * i) % 340 + 1 for i in range(S)]
     s = Step(dtype, Hkv, G, D, bs, ctx, [1] * S, seed=D + G + S)
+    ws = torch.empty(pa.pa_decode_workspace_size(S, Hkv * G, Hkv, D, max(ctx)), dtype=torch.uint8, device="cuda")
+    s.check(lambda o, q, k, v, t, st: pa.pa_decode(o, q, k, v, t, s.c, max(ctx), s.scale, workspace=ws, status=st),
+            lambda i, n, c: np.ones(c, bool), True)
     s.check(lambda o, q, k, v, t, st: pa.pa_decode_window(o, q, k, v, t, s.c, max(ctx), 100, 5, s.scale, status=st),
             lambda i, n, c: (np.arange(c) >= c - 100) | (np.arange(c) < 5), False)
     s.check(lambda o, q, k, v, t, st: pa.pa_cross_attention(o, q, None, 1, k, v, t, s.c, max(ctx), s.scale, status=st),
