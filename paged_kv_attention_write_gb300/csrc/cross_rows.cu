@@ -38,10 +38,7 @@ int launch_cross_rows(const CrossArgs &c) {
     p.token_groups = (longest - 1) / p.tokens + 1;
     const int columns = p.tokens * p.group;
     // Clusters as in decode_window.cu: the CTAs of one full wave, none with less than one stage of
-    // keys (two past eight CTAs).  In twos a ninth more than a wave pays where the contexts are ragged
-    // (164 items of up to 1333 fp32 keys 26.4 us whole, 17.5 in twos; 160 of 400 to 4000 bf16 keys 52 and
-    // 36) and costs where they are not (160 items of 4000 keys 56 and 75).  The host cannot see that;
-    // it takes ragged numbers of rows as the sign of it.
+    // keys (two past eight CTAs).
     const int sms = std::max(1, device_sm_count());
     const int64_t slots = 2 * sms, most = a.max_context_len;
     const int64_t stage_keys = 16384 / (a.head_dim * (a.kv_dtype == PA_F32 ? 4 : 2));
@@ -49,11 +46,19 @@ int launch_cross_rows(const CrossArgs &c) {
     // those that have rows: of ragged sequences some items are empty and gone at once
     const int64_t live = std::min<int64_t>(items, (p.tokens == 1 ? a.num_tokens : a.num_tokens / p.tokens + (int64_t)a.num_seqs) *
                                                       a.num_kv_heads);
-    auto fit = [&](int size) { return slots * (size == 2 ? (live < items ? 71 : 64) : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
+    auto fit = [&](int size) { return slots * (size <= 2 ? 64 : size == 4 ? 63 : size == 8 ? 61 : 48) / 64; };
     int cluster = 1;
     while (cluster < 16 && live * cluster * 2 <= fit(cluster * 2) &&
            most > stage_keys * cluster * (cluster < 8 ? 1 : 2))
         cluster *= 2;
+    // Past a wave, in twos where some items have no rows (sequences of 1 to 3 and 1 to 8 fp32 rows): their CTAs
+    // are gone at once and leave the others unevenly on the SMs, whole items more than halves.  Against whole
+    // items, 152 to 208 with rows among 192 to 290 in all: contexts of 0 to 1500 keys 0.60 to 0.80 of the
+    // time, 0 to 4000 0.55 to 0.62, 3000 to 4000 0.82 to 0.98, all of 4000 0.94 to 1.06, all of 1500 1.02 to
+    // 1.24; all of 1000 1.10 to 1.31, which is too much; 240 to 256 items of 0 to 1500 keys 0.76 to 0.99, all of
+    // 1500 1.10 to 1.23.  Without such items twos lose where contexts are alike (176 items of 1500 keys
+    // 28 -> 39 us, of 4000 64 -> 82; of 0 to 4000 60 -> 41).
+    if (cluster == 1 && live < items && live * 3 <= slots * 2 && most > 1024) cluster = 2;
     p.unit = cluster > 1 || most >= 64 * (int64_t)a.block_size ? a.block_size / 8 : 1;
     const int per_sm = (int)std::min<int64_t>(8, (live + sms - 1) / sms);
     // A warp per item where many have few keys: 320 items of 100, 250 and 500 keys (D 128) 9.7, 16 and 27 us,

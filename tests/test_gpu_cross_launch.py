@@ -1,0 +1,41 @@
+"""Cross attention where the launch goes another way: every kernel and cluster size that a call's sizes choose,
+on either side of the bounds, against the 64-bit reference.  Sizes are in parts of the chip, so that
+they go where they are meant to on any number of SMs."""
+import numpy as np
+import pytest
+import torch
+
+from cross_cases import make_case
+from test_gpu_cross import BF16, FP16, FP32, NAMES, check
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu(cuda_ok):
+    yield
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def ragged(total, most, seed):
+    """Numbers of rows, 1 to `most`, `most` among them, that sum to `total`."""
+    rng = np.random.default_rng(seed)
+    rows = [most]
+    while sum(rows) < total:
+        rows.append(min(int(rng.integers(1, most + 1)), total - sum(rows)))
+    return rows
+
+
+@pytest.mark.parametrize("most", [1024, 1025])
+@pytest.mark.parametrize("part", [0.95, 1.05, 1.3, 1.4])
+@pytest.mark.parametrize("even", [False, True], ids=["ragged", "even"])
+def test_fp32_rows_beside_empty_items(most, part, even):
+    # items with rows from a little below half a wave of CTAs to past two thirds; some more have none
+    rng = np.random.default_rng(most)
+    rows = ragged(int(part * sms()) // 4, 3, int(100 * part))
+    ctx = [most] * len(rows) if even else [most] + [int(c) for c in rng.integers(0, most, len(rows) - 1)]
+    check(make_case(FP32, 16, 4, 64, 16, ctx, rows, seed=len(rows)))
+    check(make_case(FP32, 16, 4, 64, 16, ctx, rows, "mixed", seed=len(rows)))
