@@ -1193,10 +1193,18 @@ int launch_rows(const PrefillArgs &a, const int32_t *key_ranges) {
         // listed items: a sequence's last one is half full on average
         const int64_t likely = p.listed ? (a.num_tokens / (kBM / G) + (a.num_seqs + 1) / 2) * (int64_t)a.num_kv_heads : items;
         if (likely * 4 <= sms ? keys > 384 : likely * 4 <= slots * 63 / 64 && keys > 1024) cluster = 4;
-        // Ragged contexts gain beyond that: 160 items of 100 to 3000 keys 46 us whole, 35 in twos, of 500 to
-        // 8000 keys 103 and 63; were all of 1500 keys, 33 and 44.  The host cannot see them; it takes ragged
-        // chunks as the sign of them.
-        else if (likely * 2 <= slots ? keys > 2048 : p.listed && likely <= slots * 4 / 5 && keys > 1024) cluster = 2;
+        // Beyond that twos even out items of unequal length, at the cost of the joins.  Of the time of whole
+        // items, chunks of one length and ragged ones alike, 154 to 202 items at head dimension 64 | 128:
+        // contexts of 0 to 8000 keys 0.52 to 0.61 | 0.63 to 0.65, all of 6000 0.89 to 0.90 | 0.98 to 1.03, all of
+        // 3000 1.01 to 1.02 | 1.12 to 1.18, all of 1500 1.17 to 1.20 | 1.26 to 1.33 (237 to 256 items of 3000
+        // keys 1.20 to 1.21 | 1.26 to 1.35).  Ranges make the items of equal contexts unequal too: up to 243 items
+        // beside one and four images, of 0 to 8000 keys 0.57 to 0.75 | 0.60 to 0.77, all of 6400 0.63 to 0.91 |
+        // 0.67 to 1.01, all of 3200 0.74 to 1.07 | 0.83 to 1.17, all of 1600 0.92 to 1.35 | 1.00 to 1.54 (244 to
+        // 296 items of 3200 keys 0.91 to 1.15 | 1.06 to 1.24).
+        else if (likely * 2 <= slots ? keys > 2048
+                                     : keys > 32 * (int64_t)a.head_dim &&
+                                           (key_ranges ? likely * 5 <= slots * 4 : likely * 3 <= slots * 2))
+            cluster = 2;
         while (cluster >= 4 && cluster < 16 && likely * cluster * 2 <= sms && keys > 512 * (int64_t)cluster) cluster *= 2;
     } else {
         while (cluster < 16 && items * cluster * 2 <= sms && keys > (int64_t)kBN * 4 * cluster) cluster *= 2;

@@ -39,3 +39,27 @@ def test_fp32_rows_beside_empty_items(most, part, even):
     ctx = [most] * len(rows) if even else [most] + [int(c) for c in rng.integers(0, most, len(rows) - 1)]
     check(make_case(FP32, 16, 4, 64, 16, ctx, rows, seed=len(rows)))
     check(make_case(FP32, 16, 4, 64, 16, ctx, rows, "mixed", seed=len(rows)))
+
+
+@pytest.mark.parametrize("D,bound", [(64, 2048), (128, 4096)])
+@pytest.mark.parametrize("part", [0.45, 0.62, 0.72, 0.85])
+@pytest.mark.parametrize("ranges", [None, "mixed"])
+@pytest.mark.parametrize("even", [False, True], ids=["ragged", "even"])
+def test_chunks_in_twos(D, bound, part, ranges, even):
+    # part: of the two places that an SM has.  On either side of the length, half, two thirds and four fifths
+    items = int(part * 2 * sms())
+    rows = [80] * (items // 5) if even else ragged((items - items // 14) * 16, 300, items)
+    rng = np.random.default_rng(items)
+    for most in (bound, bound + 1):
+        ctx = [most] + [int(c) for c in rng.integers(0, 400, len(rows) - 1)]
+        check(make_case(FP16 if even else BF16, 8, 1, D, 8 if D == 64 else 32, ctx, rows, ranges, seed=items + most))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("items,most", [(0.05, 4097), (0.12, 2049), (0.12, 2048), (0.24, 385), (0.24, 384), (0.45, 1025), (0.45, 1024)])
+@pytest.mark.parametrize("ranges", [None, "mixed"])
+def test_chunks_in_fours_to_sixteens(D, items, most, ranges):
+    # items: of one place per SM
+    n = int(items * sms())
+    rows = [16 * n - 37, 29] if n > 3 else [16 * n - 5]
+    check(make_case(BF16, 8, 1, D, 16, [most, 700][:len(rows)], rows, ranges, seed=n))
