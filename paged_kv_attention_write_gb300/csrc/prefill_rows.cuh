@@ -621,7 +621,8 @@ prefill_rows_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_const
             // CROSS: between the ranges of an item's rows there may be blocks that no row reaches
             auto reached = [&](int j) {
                 if constexpr (CROSS) {
-                    if (!it.holes || (j0 + j >= it.low && j0 + j < it.high) || j >= n) return true;
+                    if (j >= n) return false;  // a look ahead, past this CTA's tiles
+                    if (!it.holes || (j0 + j >= it.low && j0 + j < it.high)) return true;
                     const uint64_t seen = seen_keys(p, it, row_ranges + (k & 1) * kBM, (j0 + j) * kBN);
                     return lane < nb && (seen >> (lane << bl) & ((1ull << (1 << bl)) - 1)) != 0;
                 }

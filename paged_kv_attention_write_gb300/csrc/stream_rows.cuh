@@ -939,8 +939,11 @@ stream_rows_warp_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         if constexpr (CROSS) in = in && (!p.key_ranges || keys.reaches(8 * keys.logical(v), 8 * (keys.logical(v) + unit)));
         return in;
     };
-    // (unit 2: the id of an even group serves the next one too)
-    auto block_id = [&](int v) { return listed(v) ? bt[keys.logical(v) / per_block] : -1; };
+    // (unit 2: the id of an even group serves the next one too, so both look up the even one's)
+    auto block_id = [&](int v) {
+        v &= -unit;
+        return listed(v) ? bt[keys.logical(v) / per_block] : -1;
+    };
     // block ids of 32 groups, one per lane, and of the next 32
     int ids = block_id(lane), ids_next = block_id(32 + lane);
     Consumer16<T, D, CROSS> work(p, keys, 0, lane, s, g);
