@@ -63,3 +63,33 @@ def test_chunks_in_fours_to_sixteens(D, items, most, ranges):
     n = int(items * sms())
     rows = [16 * n - 37, 29] if n > 3 else [16 * n - 5]
     check(make_case(BF16, 8, 1, D, 16, [most, 700][:len(rows)], rows, ranges, seed=n))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=NAMES.get)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bs", [8, 16, 32])
+@pytest.mark.parametrize("per_sm,bound", [(9, 768), (6, 768), (4.5, 768), (4, 384), (2.1, 384)])
+def test_a_warp_per_item(dtype, D, bs, per_sm, bound):
+    # many items of few keys, on either side of the length up to which a warp takes each; boxes of 8 and of
+    # 16 keys; rings of three to nine (D 128) or sixteen steps, all of them walked more than once
+    Hkv, G = (8, 1) if bs == 16 else (4, 4)
+    S = int(per_sm * sms()) // Hkv
+    rng = np.random.default_rng(S)
+    for most in (bound, bound + 1):
+        ctx = [most, 0, most - 1] + [int(c) for c in rng.integers(0, 330, S - 3)]
+        if most == bound:
+            check(make_case(dtype, Hkv * G, Hkv, D, bs, ctx, [1] * S, seed=S, single=True))
+        check(make_case(dtype, Hkv * G, Hkv, D, bs, ctx, [1 + (s % 2 if G == 4 else s % 5) for s in range(S)], "mixed", seed=S + 1))
+
+
+@pytest.mark.parametrize("dtype,D", [(FP16, 64), (FP16, 128), (BF16, 128), (FP32, 128)])
+@pytest.mark.parametrize("part", [0.9, 1.2, 2.2, 4.2])
+def test_long_contexts_first(dtype, D, part):
+    # up to and past one and four waves of two CTAs per SM, of contexts too long for a warp each
+    Hkv = 8 if part > 2 else 4
+    S = int(part * 2 * sms()) // Hkv
+    rng = np.random.default_rng(S)
+    ctx = [int(c) for c in rng.integers(0, 200, S)]
+    ctx[S // 3], ctx[-1] = 1200, 900
+    check(make_case(dtype, Hkv, Hkv, D, 16, ctx, [1] * S, seed=S, single=True))
+    check(make_case(dtype, Hkv, Hkv, D, 8, ctx, [1] * S, "mixed", seed=S))
