@@ -547,9 +547,11 @@ int pa_cross_attention(void *out, pa_dtype out_dtype, const void *query, const i
  *
  * A sequence that finds too few blocks left (PA_DEVERR_FREE_LIST; no later sequence gets any
  * either), would not fit its table row or has a negative length (PA_DEVERR_CONTEXT), or whose
- * rows end past num_tokens (PA_DEVERR_QUERY) is not served: it keeps its length and table, and its
- * rows get position 0 and slot -1.  The caller sees the reported bit and runs the step
- * again with what it can serve.  A negative new length is reported (PA_DEVERR_QUERY) and taken as 0.
+ * rows end past num_tokens (PA_DEVERR_QUERY) is not served: it keeps its length (a negative one is
+ * written as 0) and table, and its rows get position 0 and slot -1.  The caller sees the reported bit
+ * and runs the step again with what it can serve.  A negative new length is reported
+ * (PA_DEVERR_QUERY) and taken as 0; a *num_free outside [0, free_capacity] is reported
+ * (PA_DEVERR_FREE_LIST) and taken as the nearer end, by pa_tables_trim too.
  * A block id outside [0, num_blocks) is reported (PA_DEVERR_BLOCK_ID); its tokens get slot -1.
  */
 int pa_tables_extend(int32_t *block_tables, int max_blocks_per_seq, int32_t *context_lens, int32_t *query_start_loc,
@@ -566,7 +568,8 @@ int pa_tables_extend(int32_t *block_tables, int max_blocks_per_seq, int32_t *con
  * free_blocks is written from *num_free on, context_lens (may be cached_lens itself) gets the
  * kept lengths, num_free_out (may be num_free itself) the new count; block_tables is only read.
  * A keep length outside [0, cached] or a cached length past the table row is reported
- * (PA_DEVERR_CONTEXT) and its sequence left as it is.  Blocks past the end of the list are
+ * (PA_DEVERR_CONTEXT) and its sequence left as it is (a negative cached length is written as 0).
+ * Blocks past the end of the list are
  * reported (PA_DEVERR_FREE_LIST) and dropped, block ids outside [0, num_blocks) reported
  * (PA_DEVERR_BLOCK_ID) and listed as they are.
  */
