@@ -490,7 +490,8 @@ int pa_reshape_and_cache_rope_axes_args(const pa_rope_axes_args *args);
  *                    chunk).  NULL: one row each, row s of sequence s, num_tokens == num_seqs
  *                    (max_query_len is not read)
  *   max_query_len    >= every sequence's rows (host bound); a sequence with more is reported
- *                    (PA_DEVERR_QUERY) and its rows left as they were
+ *                    (PA_DEVERR_QUERY) and its rows left as they were (0, like num_tokens 0: a
+ *                    no-op, which looks at no sequence)
  *   key_ranges       int32 [num_tokens][2], 8-byte aligned: (begin, end) of each row, cut to
  *                    [0, context); NULL: every row sees its whole context
  *   context_lens     int32 [num_seqs]: cached keys of the sequence, 0 allowed
