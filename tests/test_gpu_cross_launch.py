@@ -93,3 +93,25 @@ def test_long_contexts_first(dtype, D, part):
     ctx[S // 3], ctx[-1] = 1200, 900
     check(make_case(dtype, Hkv, Hkv, D, 16, ctx, [1] * S, seed=S, single=True))
     check(make_case(dtype, Hkv, Hkv, D, 8, ctx, [1] * S, "mixed", seed=S))
+
+
+@pytest.mark.parametrize("dtype,rows", [(BF16, 1), (FP32, 1), (FP16, 16)], ids=["rows", "fp32", "chunks"])
+def test_more_items_than_a_grid_holds_are_refused(dtype, rows):
+    # 65535 sequences, all but one without rows, by 65528 kv heads: 2^32 items.  Refused on the host
+    import paged_kv_attention_write_gb300 as pa
+    S, Hkv = 65535, 65528
+    q = torch.zeros((16, Hkv, 64), dtype=dtype, device="cuda")
+    kv = torch.zeros((1, 8, Hkv, 64), dtype=dtype, device="cuda")
+    starts = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    starts[-1] = rows
+    tables, ctx = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((S, 1), (S,)))
+    out = torch.full_like(q, 7.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pa.PAError) as e:
+        pa.pa_cross_attention(out, q, starts, rows, kv, kv, tables, ctx, 8, 1.0, status=status)
+    torch.cuda.synchronize()
+    assert e.value.code == -1 and status.item() == 0 and (out == 7).all()
+    # one sequence of the same heads is served
+    pa.pa_cross_attention(out, q, starts[-2:], rows, kv, kv, tables[:1], ctx[:1], 8, 1.0, status=status)
+    torch.cuda.synchronize()
+    assert status.item() == 0 and (out[:rows] == 0).all() and (out[rows:] == 7).all()
