@@ -53,7 +53,7 @@ int launch_cross_rows(const CrossArgs &c) {
         cluster *= 2;
     // Past a wave, in twos where some items have no rows (sequences of 1 to 3 and 1 to 8 fp32 rows): their CTAs
     // are gone at once and leave the others unevenly on the SMs, whole items more than halves.  Against whole
-    // items, 152 to 208 with rows among 192 to 290 in all: contexts of 0 to 1500 keys 0.60 to 0.80 of the
+    // items, 156 to 208 with rows among 216 to 320 in all: contexts of 0 to 1500 keys 0.60 to 0.80 of the
     // time, 0 to 4000 0.55 to 0.62, 3000 to 4000 0.82 to 0.98, all of 4000 0.94 to 1.06, all of 1500 1.02 to
     // 1.24; all of 1000 1.10 to 1.31, which is too much; 240 to 256 items of 0 to 1500 keys 0.76 to 0.99, all of
     // 1500 1.10 to 1.23.  Without such items twos lose where contexts are alike (176 items of 1500 keys

@@ -55,10 +55,10 @@
 // whose rows see nothing of a tile stores zero weights and is done with it.  The ranges of an item's
 // rows wait in shared memory beside its slot.  Sequences with long contexts go first, and where
 // ranges are given the last rows of all sequences, which see most of what stands before them.
-// Measured (us): fp16, 8 x 512 rows of 64 q / 8 kv heads over 4096 to 12288 keys, D 128: 842 (1.32
-// PFLOP/s; 904 in the sequences' order); bf16, 4 x 512 rows of 32 / 8 heads beside four images of 1601
-// keys: 94 (its longest items, 101 tiles, take 90); 23 ragged chunks of 8 / 1 heads beside three
-// images: 32 in clusters of two, 48 whole.  Half of each item's rows blind to all tiles but the
+// Measured (us): fp16, 8 x 512 rows of 64 q / 8 kv heads over 4096 to 12288 keys, D 128: 842 to
+// 906 as power allows (1.23 to 1.32 PFLOP/s; in the sequences' order 904 beside 842); bf16, 4 x 512
+// rows of 32 / 8 heads beside four images of 1601 keys: 94 (its longest items, 101 tiles, take 90); 23
+// ragged chunks of 8 / 1 heads beside three images: 31 in clusters of two, 48 whole.  Half of each item's rows blind to all tiles but the
 // first: 290 with scores masked one by one, 225 so, 187 when all rows see all.  A CTA per SM with the
 // warps, rings and TMEM of two, both halves on one item, was tried for items of unequal length: the
 // ragged chunks 33, 336 items of 500 to 8000 keys 134 -> 94, but the images 94 -> 96, 256 items of

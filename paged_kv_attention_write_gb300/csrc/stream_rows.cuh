@@ -53,7 +53,8 @@
 // D 128: 152 (7.0 TB/s; 194 in the sequences' order); fp16, 16 sequences of five rows over 400 to
 // 1500 keys, 16 / 16 heads, D 64: 17.2 (3.8 TB/s: an SM takes in 50 to 53 GB/s at most, and 104 of
 // them have two of the 256 items); one row over 1500 keys 6.3 (launch and the chain named above); fp32,
-// 19 sequences of 1 to 3 rows over up to 1333 keys, 16 / 4 heads: 15.6.  Tried: rings of six stages
+// 19 sequences of 1 to 3 rows over up to 1333 keys, 16 / 4 heads: 15.6 (eight columns at D 128 spill 8
+// bytes at the 168 registers that two CTAs of six warps leave).  Tried: rings of six stages
 // where an SM has one CTA (no change); for D 64, CTAs of eight consumer warps (17.9 -> 18.1), long and
 // short items on one SM (17.9 -> 18.4, the ranking), and with one producer warp four CTAs per SM on rings of half the size: 512 items of 1000 keys 34 -> 25 us, 1024 of
 // 4000 keys 180 -> 163, but 512 of 1000 to 4000 keys of one query head each 57 -> 66, 2048 of 4000
