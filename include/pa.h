@@ -570,9 +570,8 @@ int pa_tables_extend(int32_t *block_tables, int max_blocks_per_seq, int32_t *con
  * kept lengths, num_free_out (may be num_free itself) the new count; block_tables is only read.
  * A keep length outside [0, cached] or a cached length past the table row is reported
  * (PA_DEVERR_CONTEXT) and its sequence left as it is (a negative cached length is written as 0).
- * Blocks past the end of the list are
- * reported (PA_DEVERR_FREE_LIST) and dropped, block ids outside [0, num_blocks) reported
- * (PA_DEVERR_BLOCK_ID) and listed as they are.
+ * Blocks past the end of the list are reported (PA_DEVERR_FREE_LIST) and dropped, block ids outside
+ * [0, num_blocks) reported (PA_DEVERR_BLOCK_ID) and listed as they are.
  */
 int pa_tables_trim(int32_t *free_blocks, int free_capacity, int32_t *context_lens, int32_t *num_free_out,
                    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *cached_lens,

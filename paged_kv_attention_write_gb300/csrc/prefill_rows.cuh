@@ -58,10 +58,10 @@
 // Measured (us): fp16, 8 x 512 rows of 64 q / 8 kv heads over 4096 to 12288 keys, D 128: 842 to
 // 906 as power allows (1.23 to 1.32 PFLOP/s; in the sequences' order 904 beside 842); bf16, 4 x 512
 // rows of 32 / 8 heads beside four images of 1601 keys: 94 (its longest items, 101 tiles, take 90); 23
-// ragged chunks of 8 / 1 heads beside three images: 31 in clusters of two, 48 whole.  Half of each item's rows blind to all tiles but the
-// first: 290 with scores masked one by one, 225 so, 187 when all rows see all.  A CTA per SM with the
-// warps, rings and TMEM of two, both halves on one item, was tried for items of unequal length: the
-// ragged chunks 33, 336 items of 500 to 8000 keys 134 -> 94, but the images 94 -> 96, 256 items of
+// ragged chunks of 8 / 1 heads beside three images: 31 in clusters of two, 48 whole.  Half of each
+// item's rows blind to all tiles but the first: 290 with scores masked one by one, 225 so, 187 when all
+// rows see all.  A CTA per SM with the warps, rings and TMEM of two, both halves on one item, was tried for
+// items of unequal length: the ragged chunks 33, 336 items of 500 to 8000 keys 134 -> 94, but the images 94 -> 96, 256 items of
 // 6000 keys 92 -> 98 and the wide case 842 -> 912: nothing runs under an item's beginning and end.
 //
 // Warps: 0 items, TMA of Q and K, 2 of V (a lane per block), 1 issues S, 3 P.V (and clears the
